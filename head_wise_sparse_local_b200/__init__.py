@@ -18,7 +18,8 @@ import torch
 
 from . import _abi
 from ._abi import (EXPORTS, RTP_BF16, RTP_DEV_POSITION, RTP_DEV_SEQ_LEN, RTP_DEV_TIMEOUT, RTP_FP32,
-                   RTP_NOALLOC_SCRATCH_BYTES, STAGES, RtpError, rtp_cache, rtp_layer_cfg)
+                   RTP_DEV_BLOCKS, RTP_NOALLOC_SCRATCH_BYTES, STAGES, RtpError, rtp_cache, rtp_layer_cfg,
+                   rtp_q8_cache, rtp_rope_axes)
 
 _lib = _abi.load()
 
@@ -30,7 +31,9 @@ __all__ = ["Layer", "RtpError", "rtp_layer_cfg", "rtp_cache", "rtp_cache_bytes",
            "rtp_last_error", "RTP_NOALLOC_SCRATCH_BYTES",
            "rtp_version", "make_cfg", "STAGES",
            "library_path", "EXPORTS", "RTP_BF16", "RTP_FP32", "RTP_DEV_SEQ_LEN",
-           "RTP_DEV_POSITION", "RTP_DEV_TIMEOUT"]
+           "RTP_DEV_POSITION", "RTP_DEV_TIMEOUT", "RTP_DEV_BLOCKS",
+           "PagedLayer", "rtp_q8_cache", "rtp_rope_axes", "make_q8_cache", "make_rope", "rtp_q8_cache_bytes",
+           "rtp_page_plan", "rtp_append_q8", "rtp_attn_q8_workspace_bytes", "rtp_attn_q8"]
 
 
 def library_path() -> str:
@@ -152,6 +155,173 @@ def rtp_prefill_attn(cfg, cache, q_pre, start_pos, T, w_q, out, sel_bitmask=None
                                      _ptr(sel_bitmask), _ptr(sel_tau), _ptr(sel_jcut),
                                      _ptr(sel_count), _ptr(workspace), int(workspace_bytes),
                                      _stream(stream)))
+
+
+def make_q8_cache(k, v, k_scale, v_scale, status) -> rtp_q8_cache:
+    """Describe a pool of blocks: k, v [n_blocks, Hkv, block_size, D] (float8_e4m3fn or
+    uint8), scales [n_blocks, Hkv] fp32, status one int32.  It holds addresses
+    only: keep the tensors alive."""
+    if v.shape != k.shape or k.dim() != 4 or k.element_size() != 1 or v.element_size() != 1:
+        raise ValueError("k and v must be [n_blocks, Hkv, block_size, D] of one byte an element")
+    if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2] or k_scale.dtype != torch.float32 \
+            or v_scale.dtype != torch.float32:
+        raise ValueError("k_scale and v_scale must be [n_blocks, Hkv] float32")
+    return rtp_q8_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(status), k.shape[0], k.shape[2])
+
+
+def make_rope(head_dim: int, sections: Sequence[int], interleaved: bool = False) -> rtp_rope_axes:
+    """Rotary axes: axis a turns sections[a] of the head_dim / 2 rotary pairs.
+    The axes' pairs follow one another, or, interleaved, are dealt out in turn
+    (axis 0, 1, 2, 0, ...) until an axis has its number."""
+    left = [int(s) for s in sections]
+    if sum(left) != head_dim // 2 or min(left) < 0 or not 1 <= len(left) <= 4:
+        raise ValueError("one to four sections that sum to head_dim / 2")
+    r = rtp_rope_axes(len(left))
+    if interleaved:
+        k = 0
+        while k < head_dim // 2:
+            for a in range(len(left)):
+                if left[a] > 0:
+                    r.axis[k] = a
+                    left[a] -= 1
+                    k += 1
+    else:
+        r.axis[:head_dim // 2] = [a for a, s in enumerate(left) for _ in range(s)]
+    return r
+
+
+def rtp_q8_cache_bytes(cfg: rtp_layer_cfg, n_blocks: int, block_size: int):
+    kv, sc = ctypes.c_size_t(), ctypes.c_size_t()
+    _abi.check(_lib.rtp_q8_cache_bytes(ctypes.byref(cfg), int(n_blocks), int(block_size), ctypes.byref(kv),
+                                       ctypes.byref(sc)))
+    return kv.value, sc.value
+
+
+def _here(x, name) -> None:
+    """Kernels run on the current device: a tensor of another one is refused."""
+    if x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+
+
+def _arg(x, dtype, name) -> Optional[int]:
+    """_ptr of a tensor whose element type the library fixes."""
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    p = _ptr(x)
+    _here(x, name)
+    return p
+
+
+def _packed(x, cfg, heads: int, name):
+    """(address, elements between tokens) of packed [N, heads, D] rows, dense or a slice of wider rows."""
+    dt = torch.bfloat16 if cfg.dtype == RTP_BF16 else torch.float32
+    if not x.is_cuda or x.dtype != dt or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != cfg.head_dim:
+        raise ValueError(f"{name} must be a CUDA [N, {heads}, {cfg.head_dim}] tensor of {dt}")
+    _here(x, name)
+    s = x.stride()
+    if (s[2] != 1 or s[1] != cfg.head_dim) and x.numel() > 0:
+        raise ValueError(f"{name}: a token's heads must be dense")
+    return x.data_ptr(), s[0] if x.shape[0] > 1 else 0
+
+
+def _axes(pos, rope, n) -> int:
+    if pos.dtype != torch.int32 or pos.numel() != n * (rope.n_axes if rope is not None else 1):
+        raise ValueError("pos must be int32 [n_axes, N]")
+    return _arg(pos, torch.int32, "pos")
+
+
+def rtp_page_plan(cfg, block_size, ctx_len, new_len, block_table, free_list, n_free, seq_len, cu_new,
+                  slot_map, positions, n_free_out, status, stream=None) -> None:
+    i32 = torch.int32
+    cols = -(-cfg.max_ctx // block_size) if block_size > 0 else 0
+    for name, x, n in (("ctx_len", ctx_len, cfg.batch), ("new_len", new_len, cfg.batch), ("seq_len", seq_len, cfg.batch),
+                       ("cu_new", cu_new, cfg.batch + 1), ("block_table", block_table, cfg.batch * cols),
+                       ("positions", positions, slot_map.numel())):
+        if x.numel() != n:
+            raise ValueError(f"{name} must have {n} elements")
+    _abi.check(_lib.rtp_page_plan(ctypes.byref(cfg), int(block_size), _arg(ctx_len, i32, "ctx_len"),
+                                  _arg(new_len, i32, "new_len"), _arg(block_table, i32, "block_table"),
+                                  _arg(free_list, i32, "free_list"), free_list.numel(), _arg(n_free, i32, "n_free"),
+                                  _arg(seq_len, i32, "seq_len"), _arg(cu_new, i32, "cu_new"),
+                                  _arg(slot_map, torch.int64, "slot_map"), _arg(positions, i32, "positions"),
+                                  slot_map.numel(), _arg(n_free_out, i32, "n_free_out"), _arg(status, i32, "status"),
+                                  _stream(stream)))
+
+
+def rtp_append_q8(cfg, cache, k_pre, v_in, slot_map, pos, rope=None, stream=None) -> None:
+    n = k_pre.shape[0]
+    k, ks = _packed(k_pre, cfg, cfg.n_kv_heads, "k_pre")
+    v, vs = _packed(v_in, cfg, cfg.n_kv_heads, "v_in")
+    if v_in.shape[0] != n or slot_map.numel() != n:
+        raise ValueError("k_pre, v_in and slot_map must have as many tokens")
+    _abi.check(_lib.rtp_append_q8(ctypes.byref(cfg), ctypes.byref(cache), k, ks, v, vs,
+                                  _arg(slot_map, torch.int64, "slot_map"), _axes(pos, rope, n),
+                                  None if rope is None else ctypes.byref(rope), n, _stream(stream)))
+
+
+def rtp_attn_q8_workspace_bytes(cfg: rtp_layer_cfg, block_size: int, n_tokens: int, max_q: int,
+                                max_seq_len: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _abi.check(_lib.rtp_attn_q8_workspace_bytes(ctypes.byref(cfg), int(block_size), int(n_tokens), int(max_q),
+                                                int(max_seq_len), ctypes.byref(n)))
+    return n.value
+
+
+def rtp_attn_q8(cfg, cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, max_seq_len=0, rope=None,
+                workspace=None, workspace_bytes=0, stream=None) -> None:
+    n = q_pre.shape[0]
+    q, qs = _packed(q_pre, cfg, cfg.n_q_heads, "q_pre")
+    i32 = torch.int32
+    if workspace is None:
+        raise ValueError("workspace is missing: rtp_attn_q8_workspace_bytes says how much")
+    if out.shape != q_pre.shape:
+        raise ValueError("out must have q_pre's shape")
+    if cu_q.numel() != cfg.batch + 1 or seq_len.numel() != cfg.batch or \
+            block_table.numel() != cfg.batch * -(-cfg.max_ctx // cache.block_size):
+        raise ValueError("cu_q, seq_len or block_table does not fit the batch")
+    _abi.check(_lib.rtp_attn_q8(ctypes.byref(cfg), ctypes.byref(cache), q, qs, _arg(cu_q, i32, "cu_q"),
+                                _arg(seq_len, i32, "seq_len"), _arg(block_table, i32, "block_table"),
+                                _axes(pos, rope, n), None if rope is None else ctypes.byref(rope), n, int(max_q),
+                                int(max_seq_len), _arg(out, q_pre.dtype, "out"), _arg(workspace, torch.uint8, "workspace"),
+                                int(workspace_bytes), _stream(stream)))
+
+
+class PagedLayer:
+    """One layer's configuration with a pool of 8-bit blocks and scratch, all
+    torch-allocated.  Requests' block tables come from rtp_page_plan and are
+    shared by a model's layers; pass the step's to append() and attend()."""
+
+    def __init__(self, shape, max_ctx: int, n_blocks: int, block_size: int = 64, device="cuda", rope=None):
+        self.shape = shape
+        self.cfg = make_cfg(shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.head_dim, max_ctx, shape.n_sink,
+                            shape.window, 1.0, shape.retrieval, shape.dtype, shape.rope_base, shape.idx_dim)
+        rtp_q8_cache_bytes(self.cfg, n_blocks, block_size)  # refuses what the library does not take
+        self.rope = rope
+        size = (n_blocks, shape.n_kv_heads, block_size, shape.head_dim)
+        self.k = torch.zeros(size, dtype=torch.float8_e4m3fn, device=device)
+        self.v = torch.zeros(size, dtype=torch.float8_e4m3fn, device=device)
+        self.k_scale = torch.ones(size[:2], dtype=torch.float32, device=device)
+        self.v_scale = torch.ones(size[:2], dtype=torch.float32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.cache = make_q8_cache(self.k, self.v, self.k_scale, self.v_scale, self.status)
+        self.ws = torch.empty(0, dtype=torch.uint8, device=device)
+
+    def reserve(self, n_tokens: int, max_q: int, max_seq_len: int = 0) -> None:
+        """Scratch for attend() calls of that size; call it before capturing one in a graph."""
+        n = rtp_attn_q8_workspace_bytes(self.cfg, self.cache.block_size, n_tokens, max_q, max_seq_len)
+        if n > self.ws.numel():
+            self.ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+
+    def append(self, k_pre, v_in, slot_map, pos, stream=None) -> None:
+        rtp_append_q8(self.cfg, self.cache, k_pre, v_in, slot_map, pos, self.rope, stream)
+
+    def attend(self, q_pre, cu_q, seq_len, block_table, pos, out, max_q: int, max_seq_len: int = 0, stream=None) -> None:
+        self.reserve(q_pre.shape[0], max_q, max_seq_len)
+        rtp_attn_q8(self.cfg, self.cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, max_seq_len, self.rope,
+                    self.ws, self.ws.numel(), stream)
+
+    def device_status(self) -> int:
+        return int(self.status.item())
 
 
 class Layer:

@@ -17,6 +17,7 @@ RTP_ERR_CUDA = 5
 RTP_DEV_SEQ_LEN = 0x1
 RTP_DEV_POSITION = 0x2
 RTP_DEV_TIMEOUT = 0x4
+RTP_DEV_BLOCKS = 0x8
 RTP_BF16 = 0
 RTP_FP32 = 1
 RTP_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -28,11 +29,12 @@ STATUS_NAMES = {0: "RTP_OK", 1: "RTP_ERR_INVALID", 2: "RTP_ERR_SHAPE", 3: "RTP_E
 EXPORTS = ("rtp_cache_bytes", "rtp_decode_workspace_bytes", "rtp_prefill_workspace_bytes",
            "rtp_append_kv", "rtp_decode_attn", "rtp_decode_attn_noalloc", "rtp_decode_recall",
            "rtp_prefill_attn",
+           "rtp_q8_cache_bytes", "rtp_page_plan", "rtp_append_q8", "rtp_attn_q8_workspace_bytes", "rtp_attn_q8",
            "rtp_trace_stage", "rtp_debug_wait_expiry",
            "rtp_last_error", "rtp_version")
 
 STAGES = {"append": 0, "decode_score": 1, "decode_select": 2, "decode_local": 3,
-          "prefill_index": 4, "prefill_attn": 5}
+          "prefill_index": 4, "prefill_attn": 5, "page_plan": 6, "append_q8": 7, "attn_q8": 8}
 
 
 class rtp_layer_cfg(ctypes.Structure):
@@ -46,6 +48,16 @@ class rtp_layer_cfg(ctypes.Structure):
 class rtp_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kidx", ctypes.c_void_p),
                 ("status", ctypes.c_void_p)]
+
+
+class rtp_q8_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("status", ctypes.c_void_p), ("n_blocks", ctypes.c_int),
+                ("block_size", ctypes.c_int)]
+
+
+class rtp_rope_axes(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int), ("axis", ctypes.c_ubyte * 64)]
 
 
 class RtpError(RuntimeError):
@@ -78,6 +90,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rtp_debug_wait_expiry.argtypes = [i32]
     lib.rtp_decode_attn_noalloc.argtypes = [cfgp, cachep, vp, vp, i32, vp, vp, vp, vp, vp]
     lib.rtp_decode_recall.argtypes = [cfgp, cachep, vp, vp, i32, vp, vp, vp, sz, vp]
+    q8p, ropep, i64 = P(rtp_q8_cache), P(rtp_rope_axes), ctypes.c_int64
+    lib.rtp_q8_cache_bytes.argtypes = [cfgp, i32, i32, P(sz), P(sz)]
+    lib.rtp_page_plan.argtypes = [cfgp, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp]
+    lib.rtp_append_q8.argtypes = [cfgp, q8p, vp, i64, vp, i64, vp, vp, ropep, i32, vp]
+    lib.rtp_attn_q8_workspace_bytes.argtypes = [cfgp, i32, i32, i32, i32, P(sz)]
+    lib.rtp_attn_q8.argtypes = [cfgp, q8p, vp, i64, vp, vp, vp, vp, ropep, i32, i32, i32, vp, vp, sz, vp]
     for name in EXPORTS:
         getattr(lib, name).restype = ctypes.c_char_p if name in ("rtp_last_error", "rtp_version") \
             else ctypes.c_int

@@ -1,0 +1,769 @@
+// rtp_attn_q8 for few queries a request (decode, drafts to verify): one stream
+// over the paged 8-bit cache.
+//
+// Mathematics.  A query row (token t, query head g of a KV head's group) at
+// position i attends to the positions its head sees; with the stored e4m3
+// values k', v' and their block's scales ks, vs
+//   x_j = q.k'_j ks / sqrt(D) log2(e) + log2(vs),   w_j = 2^(x_j - M),
+//   O = sum_j w_j v'_j,   l = sum_j w_j / vs_j,   out = O / l.
+// Taking vs into the exponent keeps the value blocks' scales out of the
+// products and the weights in (0, 1] whatever the scales are; M is the running
+// maximum of x, moved only when a tile exceeds it by 2^8.
+//
+// Work.  A tile is 32 positions of one (request, KV head, row chunk) item.  All
+// tiles of all items form one line that is cut into equal shares, one for
+// each CTA (two an SM), so ragged batches and the short local heads load the
+// SMs evenly; an item that a cut goes through leaves one partial (O, M, l) a
+// CTA, and a second kernel joins them in order.  Inside a CTA each of 4 warps
+// takes every fourth tile and keeps its own softmax state and accumulators;
+// they meet once an item.
+//
+// A warp stages its own tiles (K and V, 2 x 32 x D bytes) three deep by TMA,
+// which also swizzles the rows for conflict-free reads; there is no barrier
+// between warps in the loop.  Products are mma.sync m16n8k16 in fp16: e4m3
+// values convert to fp16 exactly, one instruction for two.  S = Q K^T takes Q
+// as the 16-row operand: 8 rows as a high and a low fp16 part (22 bits), or 16
+// rows in one part where there are more.  Its accumulator layout is the layout
+// the second product wants the weights in, O^T = V^T W^T with V^T read
+// transposed by byte-wise ldmatrix.
+//
+// Bound: memory.  128 positions of K and V are 32 KB; at 6.5 TB/s an SM gets
+// 23 B a clock, so 1400 clocks; the products are 192 mma.sync of 2 clocks each and 512
+// conversions of about 1 clock.  (tcgen05 would spend as long: its 128-row operand would be
+// 8 or 16 rows full.)
+#include "q8.cuh"
+#include "tensor_map.h"
+
+namespace rtp {
+namespace {
+
+constexpr int kAqWarps = 4;
+constexpr int kAqThreads = kAqWarps * 32;
+constexpr int kAqTile = 32;   // positions a tile
+constexpr int kAqStages = 3;  // tiles in flight a warp
+constexpr int kAqCtasPerSm = 2;
+constexpr float kAqRescale = 8.f;  // M moves when a tile exceeds it by 2^8
+constexpr float kAqLift = 6.f;     // weights are held 2^6 up (at most 2^14 in fp16), away from fp16's small end
+
+struct __align__(64) AttnQ8Args {
+  CUtensorMap tm_k, tm_v;  // the pool as [n_blocks Hkv block_size][D] bytes, boxes of min(32, block_size) rows
+  Q8Pool pool;
+  RopeAxes rope;
+  int B, Hq, Hkv, G, S, W, rows, n_cta;
+  long long n_slots;  // partials that the workspace holds
+  uint64_t ret_mask;
+  AttnQ8Call c;
+  float* part;  // [n_cta + items][rows][D] O, then [..][rows][2] (M, l)
+  float* part_ml;
+  unsigned long long wait_ns;
+  double inv_freq[64];
+};
+
+// A request's queries and tiles.
+struct ReqQ8 {
+  int q0, n, L;   // first packed row, queries, cached positions
+  int rc;         // row chunks
+  int tr, tl;     // tiles of a retrieval and of a local KV head
+  int ns, w0;     // a local head's tiles: [0, ns) and [w0, tr)
+  __device__ __forceinline__ long long tiles(int R, int Hkv) const {
+    return (long long)rc * ((long long)R * tr + (long long)(Hkv - R) * tl);
+  }
+};
+
+__device__ __forceinline__ ReqQ8 load_req(const AttnQ8Args& a, int b, int& flags) {
+  ReqQ8 r = {};
+  const int q0 = a.c.cu_q[b], q1 = a.c.cu_q[b + 1], L = a.c.seq_len[b];
+  const long long n = (long long)q1 - q0;
+  if (n < 0 || n > a.c.max_q || q0 < 0 || q1 > a.c.n_tokens) {
+    flags |= RTP_DEV_POSITION;
+    return r;
+  }
+  if (n == 0) return r;
+  if (L < n || L > a.c.max_seq_len) {
+    flags |= RTP_DEV_SEQ_LEN;
+    return r;
+  }
+  r.q0 = q0;
+  r.n = (int)n;
+  r.L = L;
+  r.rc = (int)((n * a.G + a.rows - 1) / a.rows);
+  r.tr = (L - 1) / kAqTile + 1;
+  r.ns = min((a.S + kAqTile - 1) / kAqTile, r.tr);
+  r.w0 = max(0, L - r.n - a.W + 1) / kAqTile;
+  if (r.w0 <= r.ns) {
+    r.ns = r.w0 = 0;
+    r.tl = r.tr;
+  } else {
+    r.tl = r.ns + r.tr - r.w0;
+  }
+  return r;
+}
+
+__device__ __forceinline__ long long warp_sum_ll(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ long long warp_scan_ll(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  return v;
+}
+
+// All tiles of the call (every warp for itself).
+__device__ __forceinline__ long long total_tiles(const AttnQ8Args& a, int R, int& flags) {
+  long long t = 0;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) t += load_req(a, b, flags).tiles(R, a.Hkv);
+  return warp_sum_ll(t);
+}
+
+// Tiles a CTA takes: an equal share, at least one a warp.
+__device__ __forceinline__ long long share_of(const AttnQ8Args& a, long long total) {
+  return max((total + a.n_cta - 1) / a.n_cta, (long long)kAqWarps);
+}
+
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* tm, int y, uint64_t* bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(0), "r"(y), "l"(pol)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two 16 x 16 byte matrices, transposed: rows at the 32 lanes' addresses (16
+// bytes each, lanes 0-15 the first matrix).  Lane l gets of each matrix the
+// bytes of rows 4 (l % 4) .. + 3 in columns l / 4 and l / 4 + 8.
+__device__ __forceinline__ void ldsm_b8_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// What a tile's consumers need beside its rows; the scales arrive by cp.async.
+struct __align__(16) TileMeta {
+  float ks[2], vs[2];  // scales of its first and second 16 positions
+  int there;           // bit q: those 16 positions' block is in the pool
+};
+
+template <int D, int ROWS>
+struct AqSmem {
+  static constexpr int kStage = 2 * kAqTile * D;                       // K, then V
+  static constexpr int kRing = kAqWarps * kAqStages * kStage;
+  static constexpr int kQPitch = D + 4;
+  static constexpr int kOffQ = kRing;                                  // rotated queries, fp32
+  static constexpr int kOffMeta = kOffQ + ROWS * kQPitch * 4;
+  static constexpr int kBytes = kOffMeta + kAqWarps * kAqStages * (int)sizeof(TileMeta) + 1024;
+  static constexpr int kMPitch = D + 2;                                // joining the warps: O rows, M, l (over the ring)
+  static_assert(kAqWarps * ROWS * kMPitch * 4 <= kRing, "the warps' partials fit in the ring");
+};
+
+// out = O / l of one row element.
+template <typename T>
+__device__ __forceinline__ T finish(float o, float l) {
+  return from_f32<T>(l == 0.f ? 0.f : o / l);  // l = 0: no position of the row is there
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const __grid_constant__ AttnQ8Args a) {
+  using SM = AqSmem<D, ROWS>;
+  constexpr bool kTwoParts = ROWS == 8;          // queries as high + low fp16 parts
+  constexpr bool kWLow = sizeof(T) == 4;         // weights as well (fp32 layers)
+  constexpr int NR = ROWS / 8;                   // rows a lane quad holds scores of; column groups of O^T
+  constexpr int KS = D / 16;
+  static_assert(!kWLow || kTwoParts, "fp32 layers run 8 rows");
+  extern __shared__ __align__(1024) unsigned char dsm_raw[];
+  __shared__ __align__(8) uint64_t s_bar[kAqWarps][kAqStages];
+  __shared__ float s_qs[ROWS];  // per row: factor from products to base-2 logits
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  unsigned char* dsm = dsm_raw + ((1024u - (smem_u32(dsm_raw) & 1023u)) & 1023u);
+  unsigned char* ring = dsm + warp * kAqStages * SM::kStage;
+  float* s_q = reinterpret_cast<float*>(dsm + SM::kOffQ);
+  TileMeta* meta = reinterpret_cast<TileMeta*>(dsm + SM::kOffMeta) + warp * kAqStages;
+  uint64_t* bar = s_bar[warp];
+  if (tid == 0) {
+    // two arrivals a phase: the copies' expect_tx and the scales' cp.async
+    for (int w = 0; w < kAqWarps; ++w)
+      for (int s = 0; s < kAqStages; ++s) mbar_init(&s_bar[w][s], 2);
+    s_abort = 0;
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch();
+
+  const int R = __popcll(a.ret_mask);
+  int flags = 0;
+  const long long total = total_tiles(a, R, flags);
+  if (blockIdx.x == 0 && warp == 0 && flags) atomicOr(a.pool.status, flags);
+  const long long share = share_of(a, total);
+  long long at = (long long)blockIdx.x * share;
+  const long long end = min(total, at + share);
+  if (at >= end) return;  // uniform
+  // ---- the request that holds tile `at`: tiles and items ahead of it ----
+  int b = 0;
+  long long b_tiles = 0, b_items = 0;
+  for (int b0 = 0;; b0 += 32) {
+    int dummy = 0;
+    ReqQ8 r = {};
+    if (b0 + lane < a.B) r = load_req(a, b0 + lane, dummy);
+    const long long t = r.tiles(R, a.Hkv), it = (long long)r.rc * a.Hkv;
+    const long long ts = warp_scan_ll(t), is = warp_scan_ll(it);
+    const unsigned m = __ballot_sync(0xffffffffu, b_tiles + ts > at);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      b = b0 + l;
+      b_tiles += __shfl_sync(0xffffffffu, ts - t, l);
+      b_items += __shfl_sync(0xffffffffu, is - it, l);
+      break;
+    }
+    b_tiles += __shfl_sync(0xffffffffu, ts, 31);
+    b_items += __shfl_sync(0xffffffffu, is, 31);
+  }
+
+  const uint64_t pol = l2_evict_first();
+  const int bs1 = (1 << a.pool.log_bs) - 1;
+  const bool split = a.pool.log_bs == 4;  // a tile is two blocks
+  int st = 0;        // ring position of the next tile to consume,
+  uint32_t ph = 0u;  // and its phase
+  ReqQ8 rq = load_req(a, b, flags);
+
+  while (at < end) {
+    // ---- the segment: tiles [u0, u1) of item (b, h, rch) ----
+    long long rel = at - b_tiles;
+    while (rel >= rq.tiles(R, a.Hkv)) {  // on to the next request that has tiles
+      b_tiles += rq.tiles(R, a.Hkv);
+      b_items += (long long)rq.rc * a.Hkv;
+      rel = at - b_tiles;
+      rq = load_req(a, ++b, flags);
+    }
+    int h = 0;
+    bool ret = a.ret_mask & 1ull;
+    int nt = ret ? rq.tr : rq.tl;
+    while (rel >= (long long)nt * rq.rc) {
+      rel -= (long long)nt * rq.rc;
+      ++h;
+      ret = (a.ret_mask >> h) & 1ull;
+      nt = ret ? rq.tr : rq.tl;
+    }
+    const int rch = (int)(rel / nt);
+    const int u0 = (int)(rel - (long long)rch * nt);
+    const int u1 = (int)min((long long)nt, u0 + (end - at));
+    const long long item = b_items + (long long)h * rq.rc + rch;
+    const int row0 = rch * ROWS, n_rows = min(ROWS, rq.n * a.G - row0);
+    const int i0 = rq.L - rq.n;                            // position of the request's first query
+    const int i_lo = i0 + row0 / a.G, i_hi = i0 + (row0 + n_rows - 1) / a.G;  // of this chunk's rows
+    const int* tab = a.c.block_table + (size_t)b * a.pool.table_cols;
+    const int mine = u0 + warp < u1 ? (u1 - u0 - warp + kAqWarps - 1) / kAqWarps : 0;  // this warp's tiles
+
+    auto tile_key = [&](int n) {  // first position of the warp's n-th tile
+      const int u = u0 + warp + n * kAqWarps;
+      return (ret || u < rq.ns ? u : rq.w0 + u - rq.ns) * kAqTile;
+    };
+    // ids of the blocks of a tile's two halves (lane 0)
+    auto block_ids = [&](int n, int (&id)[2]) {
+      const int j0 = tile_key(n);
+      const int c0 = j0 >> a.pool.log_bs;
+      id[0] = tab[c0];
+      id[1] = split ? (j0 + 16 < rq.L ? tab[c0 + 1] : -1) : id[0];
+    };
+    auto issue = [&](int n, int s, const int (&id)[2]) {  // lane 0: tile n into ring stage s
+      const int j0 = tile_key(n);
+      int there = 0, y[2], blk[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool in = (unsigned)id[q] < (unsigned)a.pool.n_blocks;
+        if (!in && j0 + 16 * q < rq.L) flags |= RTP_DEV_BLOCKS;
+        there |= (in ? 1 : 0) << q;
+        blk[q] = in ? id[q] : 0;
+        y[q] = ((blk[q] * a.Hkv + h) << a.pool.log_bs) + (split ? 0 : j0 & bs1);
+      }
+      TileMeta* m = meta + s;
+      m->there = there;
+      unsigned char* dst = ring + s * SM::kStage;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const size_t bh = (size_t)blk[q] * a.Hkv + h;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(&m->ks[q])), "l"(a.pool.k_scale + bh) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(&m->vs[q])), "l"(a.pool.v_scale + bh) : "memory");
+      }
+      cp_async_arrive_noinc(&bar[s]);
+      mbar_expect_tx(&bar[s], (uint32_t)SM::kStage);
+      tma_tile(dst, &a.tm_k, y[0], &bar[s], pol);
+      if (split) tma_tile(dst + 16 * D, &a.tm_k, y[1], &bar[s], pol);
+      tma_tile(dst + kAqTile * D, &a.tm_v, y[0], &bar[s], pol);
+      if (split) tma_tile(dst + kAqTile * D + 16 * D, &a.tm_v, y[1], &bar[s], pol);
+    };
+    int next_id[2] = {0, 0};  // blocks of the next tile to issue
+    if (lane == 0) {
+      int s = st;
+#pragma unroll
+      for (int n = 0; n < kAqStages; ++n) {
+        if (n < mine) {
+          int id[2];
+          block_ids(n, id);
+          issue(n, s, id);
+        }
+        s = s + 1 == kAqStages ? 0 : s + 1;
+      }
+      if (mine > kAqStages) block_ids(kAqStages, next_id);
+    }
+
+    // ---- queries: rotated in fp32, then as fp16 operands of a power-of-two scale a row ----
+    for (int task = tid; task < ROWS * (D / 2); task += kAqThreads) {
+      const int r = task / (D / 2), k = task % (D / 2);
+      float y1 = 0.f, y2 = 0.f;
+      if (r < n_rows) {
+        const int tok = rq.q0 + (row0 + r) / a.G, hq = h * a.G + (row0 + r) % a.G;
+        const T* q = static_cast<const T*>(a.c.q_pre) + (size_t)tok * a.c.q_stride + (size_t)hq * D;
+        const float x1 = to_f32(q[k]), x2 = to_f32(q[k + D / 2]);
+        float c, s;
+        rope_cos_sin(a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + tok], a.inv_freq[k], c, s);
+        y1 = x1 * c - x2 * s;
+        y2 = x2 * c + x1 * s;
+      }
+      s_q[r * SM::kQPitch + k] = y1;
+      s_q[r * SM::kQPitch + k + D / 2] = y2;
+    }
+    __syncthreads();
+    for (int r = warp; r < ROWS; r += kAqWarps) {
+      float m = 0.f;
+      for (int k = lane; k < D; k += 32) m = fmaxf(m, fabsf(s_q[r * SM::kQPitch + k]));
+      m = warp_max(m);
+      // row scale 2^e with |q| 2^-e < 2^9: the low part keeps 11 more bits above fp16's smallest step
+      int e = (int)(__float_as_uint(m) >> 23) - 127 - 8;
+      e = m == 0.f ? 0 : min(max(e, -100), 110);
+      if (lane == 0) s_qs[r] = __uint_as_float((uint32_t)(e + 127) << 23);
+    }
+    __syncthreads();
+    uint32_t qa[KS][4];
+    float sc[NR];
+    {
+      const float inv0 = 1.f / s_qs[g];
+      const float inv1 = kTwoParts ? inv0 : 1.f / s_qs[(g + 8) % ROWS];
+      const float unit = 1.4426950408889634f * rsqrtf((float)D);
+      sc[0] = s_qs[g] * unit;
+      if constexpr (NR == 2) sc[1] = s_qs[g + 8] * unit;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(s_q + g * SM::kQPitch + t4 * (D / 4) + 4 * j);
+        const float v[4] = {x.x * inv0, x.y * inv0, x.z * inv0, x.w * inv0};
+        qa[j][0] = pack_f16(v[0], v[1]);
+        qa[j][2] = pack_f16(v[2], v[3]);
+        if constexpr (kTwoParts) {
+          float lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) lo[e] = v[e] - __half2float(__float2half_rn(v[e]));
+          qa[j][1] = pack_f16(lo[0], lo[1]);
+          qa[j][3] = pack_f16(lo[2], lo[3]);
+        } else {
+          const float4 y = *reinterpret_cast<const float4*>(s_q + (g + 8) * SM::kQPitch + t4 * (D / 4) + 4 * j);
+          qa[j][1] = pack_f16(y.x * inv1, y.y * inv1);
+          qa[j][3] = pack_f16(y.z * inv1, y.w * inv1);
+        }
+      }
+    }
+    int pi[NR];  // position of the lane's score rows (-1: no such row)
+#pragma unroll
+    for (int r = 0; r < NR; ++r) pi[r] = g + 8 * r < n_rows ? i0 + (row0 + g + 8 * r) / a.G : -1;
+
+    // ---- the stream ----
+    float o[KS][NR][4];
+    float M[NR], l[NR];
+#pragma unroll
+    for (int m = 0; m < KS; ++m)
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[m][r][e] = 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      M[r] = -CUDART_INF_F;
+      l[r] = 0.f;
+    }
+    int n = 0;
+    for (; n < mine; ++n) {
+      const bool ok = mbar_wait_bounded(&bar[st], ph, a.wait_ns, a.pool.status);
+      if (!__all_sync(0xffffffffu, ok)) {
+        s_abort = 1;
+        break;
+      }
+      const unsigned char* kt = ring + st * SM::kStage;
+      const uint32_t vt = smem_u32(kt + kAqTile * D);
+      const TileMeta m = meta[st];
+      const int j0 = tile_key(n);
+      // S = Q K^T: column c of product u is position 16 (u/2) + 4 (c/2) + 2 (u%2) + c%2
+      float s[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+        const int kr = 16 * (u >> 1) + 4 * (g >> 1) + 2 * (u & 1) + (g & 1);
+        uint32_t w[D / 16];
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(kt + kr * 128 + (((2 * t4) ^ (kr & 7)) << 4));
+          const uint4 y = *reinterpret_cast<const uint4*>(kt + kr * 128 + (((2 * t4 + 1) ^ (kr & 7)) << 4));
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+          w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+        } else {
+          const uint4 x = *reinterpret_cast<const uint4*>(kt + kr * 64 + ((t4 ^ ((kr >> 1) & 3)) << 4));
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        }
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+          mma_f16(s[u], qa[j][0], qa[j][1], qa[j][2], qa[j][3], e4m3x2_to_f16x2(w[j]), e4m3x2_to_f16x2(w[j] >> 16));
+      }
+      // base-2 logits with the value scale's exponent
+      const float lv[2] = {__log2f(fmaxf(m.vs[0], kQ8ScaleMin)), __log2f(fmaxf(m.vs[1], kQ8ScaleMin))};
+      float x[NR][8];  // [2 u + e]
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float f = sc[r] * fmaxf(m.ks[u >> 1], kQ8ScaleMin);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            x[r][2 * u + e] = fmaf(kTwoParts ? s[u][e] + s[u][2 + e] : s[u][2 * r + e], f, lv[u >> 1]);
+        }
+      // every position there and seen by every row?
+      const bool all_there = m.there == 3 && j0 + kAqTile - 1 <= i_hi;
+      const bool whole =
+          all_there && j0 + kAqTile - 1 <= i_lo && (ret || j0 + kAqTile - 1 < a.S || j0 > i_hi - a.W);
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = j0 + 16 * (u >> 1) + 4 * t4 + 2 * (u & 1) + e;
+              const bool see = j <= pi[r] && (m.there >> (u >> 1) & 1) && (ret || j < a.S || j > pi[r] - a.W);
+              x[r][2 * u + e] = see ? x[r][2 * u + e] : -CUDART_INF_F;
+            }
+      }
+      float mx[NR];
+      bool move = false;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        mx[r] = x[r][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) mx[r] = fmaxf(mx[r], x[r][e]);
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        move = move || mx[r] > M[r] + kAqRescale || (M[r] == -CUDART_INF_F && mx[r] > M[r]);
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float mn = fmaxf(M[r], mx[r]);
+          const float f = M[r] == -CUDART_INF_F ? 0.f : ex2(M[r] - mn);
+          M[r] = mn;
+          l[r] *= f;
+          // O^T's columns are rows 2 t4 and 2 t4 + 1 of the row group
+          const float f0 = __shfl_sync(0xffffffffu, f, 8 * t4), f1 = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            o[k][r][0] *= f0;
+            o[k][r][1] *= f1;
+            o[k][r][2] *= f0;
+            o[k][r][3] *= f1;
+          }
+        }
+      }
+      uint32_t wh[2][NR][2], wl[2][NR][2];  // [16 positions][row group][b0, b1]
+      const float rv[2] = {ex2(-lv[0]), ex2(-lv[1])};
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float sub = kAqLift - (M[r] == -CUDART_INF_F ? 0.f : M[r]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = ex2(x[r][4 * q + e] + sub);
+          l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), rv[q], l[r]);
+          wh[q][r][0] = pack_f16(w[0], w[1]);
+          wh[q][r][1] = pack_f16(w[2], w[3]);
+          if constexpr (kWLow) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] -= __half2float(__float2half_rn(w[e]));
+            wl[q][r][0] = pack_f16(w[0], w[1]);
+            wl[q][r][1] = pack_f16(w[2], w[3]);
+          }
+        }
+      }
+      // O^T += V^T W^T; rows of V that are not there may hold anything: zero (0 x NaN is not 0)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t keep = 0xffffffffu;
+        if (!all_there) {
+          keep = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((m.there >> q & 1) && j0 + 16 * q + 4 * t4 + e <= i_hi) keep |= 0xffu << (8 * e);
+        }
+        const int vr = 16 * q + (lane & 15);
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          const int c = k + (lane >> 4);
+          uint32_t v[4];
+          ldsm_b8_t(v, D == 128 ? vt + vr * 128 + ((c ^ (vr & 7)) << 4) : vt + vr * 64 + ((c ^ ((vr >> 1) & 3)) << 4));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] &= keep;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t a0 = e4m3x2_to_f16x2(v[2 * p]), a2 = e4m3x2_to_f16x2(v[2 * p] >> 16);
+            const uint32_t a1 = e4m3x2_to_f16x2(v[2 * p + 1]), a3 = e4m3x2_to_f16x2(v[2 * p + 1] >> 16);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              mma_f16(o[k + p][r], a0, a1, a2, a3, wh[q][r][0], wh[q][r][1]);
+              if constexpr (kWLow) mma_f16(o[k + p][r], a0, a1, a2, a3, wl[q][r][0], wl[q][r][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0 && n + kAqStages < mine) {
+        const int id[2] = {next_id[0], next_id[1]};
+        if (n + kAqStages + 1 < mine) block_ids(n + kAqStages + 1, next_id);
+        issue(n + kAqStages, st, id);
+      }
+      if (++st == kAqStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+    if (n < mine) {  // gave up: let the copies in flight land before anything else
+      for (int k = n; k < min(mine, n + kAqStages); ++k) {
+        mbar_wait_bounded(&bar[st], ph, a.wait_ns, a.pool.status);
+        if (++st == kAqStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // ---- join the warps (their partials over the ring, once every warp is done with it) ----
+    __syncthreads();
+    if (s_abort) break;  // uniform
+    float* mg = reinterpret_cast<float*>(dsm);
+    {
+      float* mw = mg + warp * ROWS * SM::kMPitch;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (t4 == 0) {
+          mw[(g + 8 * r) * SM::kMPitch + D] = M[r];
+          mw[(g + 8 * r) * SM::kMPitch + D + 1] = l[r];
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mw[(8 * r + 2 * t4 + (e & 1)) * SM::kMPitch + k * 16 + g + 8 * (e >> 1)] = o[k][r][e];
+      }
+    }
+    __syncthreads();
+    const bool alone = u0 == 0 && u1 == nt;  // the whole item is here
+    const long long slot = blockIdx.x + item;
+    for (int i = tid; i < n_rows * D; i += kAqThreads) {
+      const int r = i / D, d = i % D;
+      const float* p = mg + r * SM::kMPitch;
+      float m = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < kAqWarps; ++w) m = fmaxf(m, p[w * ROWS * SM::kMPitch + D]);
+      const float ms = m == -CUDART_INF_F ? 0.f : m;
+      float os = 0.f, ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAqWarps; ++w) {
+        const float f = ex2(p[w * ROWS * SM::kMPitch + D] - ms);
+        os = fmaf(p[w * ROWS * SM::kMPitch + d], f, os);
+        ls = fmaf(p[w * ROWS * SM::kMPitch + D + 1], f, ls);
+      }
+      if (alone) {
+        const int tok = rq.q0 + (row0 + r) / a.G, hq = h * a.G + (row0 + r) % a.G;
+        static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + d] = finish<T>(os, ls);
+      } else if (slot < a.n_slots) {  // always, unless cu_q goes back and forth
+        a.part[((size_t)slot * ROWS + r) * D + d] = os;
+        if (d == 0) {
+          a.part_ml[((size_t)slot * ROWS + r) * 2] = m;
+          a.part_ml[((size_t)slot * ROWS + r) * 2 + 1] = ls;
+        }
+      }
+    }
+    fence_async_smem();  // the ring held ordinary stores; the next segment's copies overwrite them
+    __syncthreads();
+    at += u1 - u0;
+  }
+  if (lane == 0 && flags) atomicOr(a.pool.status, flags);
+}
+
+// Joins the partials of the items that more than one CTA worked on: one CTA an
+// item and row, one thread a dim, the partials in their order.
+template <typename T, int D>
+__global__ void __launch_bounds__(D) attn_q8_join_kernel(const __grid_constant__ AttnQ8Args a) {
+  griddep_wait();
+  const int R = __popcll(a.ret_mask), lane = threadIdx.x & 31;
+  int flags = 0;
+  // item blockIdx.x: its request, KV head and row chunk (every warp for itself)
+  long long before_t = 0, before_i = 0, total = 0;
+  int b = -1;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    ReqQ8 r = {};
+    if (b0 + lane < a.B) r = load_req(a, b0 + lane, flags);
+    const long long t = r.tiles(R, a.Hkv), it = (long long)r.rc * a.Hkv;
+    const long long ts = warp_scan_ll(t), is = warp_scan_ll(it);
+    if (b < 0) {
+      const unsigned m = __ballot_sync(0xffffffffu, before_i + is > (long long)blockIdx.x);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        b = b0 + l;
+        before_t = total + __shfl_sync(0xffffffffu, ts - t, l);
+        before_i += __shfl_sync(0xffffffffu, is - it, l);
+      } else {
+        before_i += __shfl_sync(0xffffffffu, is, 31);
+      }
+    }
+    total += __shfl_sync(0xffffffffu, ts, 31);
+  }
+  if (b < 0) return;
+  const ReqQ8 rq = load_req(a, b, flags);
+  const long long share = share_of(a, total);
+  const int ii = (int)(blockIdx.x - before_i), h = ii / rq.rc, rch = ii % rq.rc;
+  const int r = blockIdx.y, row = rch * a.rows + r;
+  if (row >= rq.n * a.G) return;
+  const int rb = __popcll(a.ret_mask & ((1ull << h) - 1ull));  // retrieval heads ahead of h
+  const int nt = (a.ret_mask >> h) & 1ull ? rq.tr : rq.tl;
+  const long long t0 = before_t + (long long)rq.rc * ((long long)rb * rq.tr + (long long)(h - rb) * rq.tl) + (long long)rch * nt;
+  const int c0 = (int)(t0 / share), c1 = (int)((t0 + nt - 1) / share);
+  if (c0 == c1) return;  // one CTA did it all and wrote the result
+  const float* ml = a.part_ml + (((size_t)blockIdx.x + c0) * a.rows + r) * 2;
+  const float* po = a.part + (((size_t)blockIdx.x + c0) * a.rows + r) * D + threadIdx.x;
+  const int np = c1 - c0 + 1;
+  float m = -CUDART_INF_F;
+  for (int p = lane; p < np; p += 32) m = fmaxf(m, ml[(size_t)p * a.rows * 2]);
+  m = warp_max(m);
+  const float ms = m == -CUDART_INF_F ? 0.f : m;
+  float os = 0.f, ls = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < np; ++p) {
+    const float f = ex2(ml[(size_t)p * a.rows * 2] - ms);
+    os = fmaf(po[(size_t)p * a.rows * D], f, os);
+    ls = fmaf(ml[(size_t)p * a.rows * 2 + 1], f, ls);
+  }
+  const int tok = rq.q0 + row / a.G, hq = h * a.G + row % a.G;
+  static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + threadIdx.x] = finish<T>(os, ls);
+}
+
+// Query rows of an item: 8 (queries in two fp16 parts) for fp32 layers and
+// where a KV head's rows fit in 8, else 16.
+int item_rows(const Shape& sh, int max_q) { return sh.dtype == RTP_FP32 || (long long)max_q * sh.G <= 8 ? 8 : 16; }
+
+long long max_items(const Shape& sh, int n_tokens, int max_q, int rows) {
+  // sum over requests of ceil(n G / rows)
+  const long long reqs = sh.B < n_tokens ? sh.B : n_tokens;
+  const long long by_tokens = (long long)n_tokens * sh.G / rows + reqs;
+  const long long by_max = reqs * (((long long)max_q * sh.G + rows - 1) / rows);
+  return sh.Hkv * (by_tokens < by_max ? by_tokens : by_max);
+}
+
+constexpr int kAqMaxCtas = 148 * kAqCtasPerSm;  // every SM of a B200
+
+template <typename T, int D, int ROWS>
+cudaError_t launch(const AttnQ8Args& a, long long items, cudaStream_t st) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int smem = AqSmem<D, ROWS>::kBytes;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(attn_q8_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  e = launch_pdl(attn_q8_kernel<T, D, ROWS>, dim3(a.n_cta), dim3(kAqThreads), smem, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_q8_join_kernel<T, D>, dim3((unsigned)items, ROWS), dim3(D), 0, st, a);
+}
+
+}  // namespace
+
+size_t attn_q8_workspace_bytes(const Shape& sh, int log_bs, int n_tokens, int max_q, int max_seq_len) {
+  (void)log_bs;
+  (void)max_seq_len;
+  const int rows = item_rows(sh, max_q);
+  const size_t slots = (size_t)kAqMaxCtas + (size_t)max_items(sh, n_tokens, max_q, rows);
+  const size_t bytes = slots * rows * (sh.D + 2) * sizeof(float);
+  return (bytes + 255) / 256 * 256;
+}
+
+int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, const AttnQ8Call& c, void* ws,
+                   cudaStream_t st) {
+  AttnQ8Args a;
+  const unsigned long long rows = ((unsigned long long)pool.n_blocks * sh.Hkv) << pool.log_bs;
+  const unsigned box = pool.log_bs == 4 ? 16 : kAqTile;
+  const CUtensorMapSwizzle sw = sh.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!make_tensor_map(&a.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool.k, sh.D, rows, sh.D, box, sw,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !make_tensor_map(&a.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool.v, sh.D, rows, sh.D, box, sw,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B)) {
+    set_error("attn q8: could not encode the K/V tensor maps (cuTensorMapEncodeTiled)");
+    return RTP_ERR_CUDA;
+  }
+  a.pool = pool;
+  a.rope = rope;
+  a.B = sh.B; a.Hq = sh.Hq; a.Hkv = sh.Hkv; a.G = sh.G; a.S = sh.S; a.W = sh.W;
+  a.ret_mask = 0;
+  for (int h = 0; h < sh.Hkv; ++h)
+    if (sh.ret_rank[h] >= 0) a.ret_mask |= 1ull << h;
+  a.c = c;
+  a.rows = item_rows(sh, c.max_q);
+  a.wait_ns = 400ull * 1000 * 1000;
+  for (int i = 0; i < 64; ++i) a.inv_freq[i] = sh.inv_freq[i];
+  const long long items = max_items(sh, c.n_tokens, c.max_q, a.rows);
+  a.n_cta = kAqMaxCtas;
+  a.part = static_cast<float*>(ws);
+  a.n_slots = kAqMaxCtas + items;
+  a.part_ml = a.part + (size_t)a.n_slots * a.rows * sh.D;
+  cudaError_t e;
+  trace_begin(RTP_STAGE_ATTN_Q8, st);
+  if (sh.dtype == RTP_BF16) {
+    if (a.rows == 8) e = sh.D == 128 ? launch<__nv_bfloat16, 128, 8>(a, items, st) : launch<__nv_bfloat16, 64, 8>(a, items, st);
+    else e = sh.D == 128 ? launch<__nv_bfloat16, 128, 16>(a, items, st) : launch<__nv_bfloat16, 64, 16>(a, items, st);
+  } else {
+    e = sh.D == 128 ? launch<float, 128, 8>(a, items, st) : launch<float, 64, 8>(a, items, st);
+  }
+  trace_end(RTP_STAGE_ATTN_Q8, st);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    set_error(std::string("attn q8 launch: ") + cudaGetErrorString(e));
+    return RTP_ERR_CUDA;
+  }
+  return RTP_OK;
+}
+
+}  // namespace rtp

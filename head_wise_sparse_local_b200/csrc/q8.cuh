@@ -1,0 +1,39 @@
+// Device helpers of the paged 8-bit cache.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "q8.h"
+
+namespace rtp {
+
+constexpr float kQ8ScaleMin = 5.42101086242752217e-20f;  // 2^-64, the smallest block scale
+
+// Two e4m3 values (low byte first) as fp16, exactly; the upper half of `two` is ignored.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+// Nearest e4m3 values (ties to even) of two floats, lo in the low byte.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Least power of two s >= 2^-64 with a <= 448 s, for finite a >= 0.  448 is
+// 1.75 * 2^8: with a = m 2^e, s is 2^(e-8) where m <= 1.75 and 2^(e-7) above.
+__device__ __forceinline__ float q8_scale(float a) {
+  const uint32_t u = __float_as_uint(a);
+  int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, 127 - 64);
+  return __uint_as_float((uint32_t)e << 23);
+}
+
+// 1 / s of a power of two 2^-64 <= s <= 2^121, exactly.
+__device__ __forceinline__ float q8_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+}  // namespace rtp

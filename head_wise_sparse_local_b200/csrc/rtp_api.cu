@@ -114,8 +114,19 @@ int make_shape(const rtp_layer_cfg* cfg, Shape* sh) {
   }
   if (rows > INT32_MAX) return fail(RTP_ERR_SHAPE, "cache rows per sequence exceed 2^31");
   sh->kv.rows_per_seq = rows;
-  for (int k = 0; k < 64; ++k)
-    sh->inv_freq[k] = k < sh->D / 2 ? std::pow((double)sh->rope_base, -2.0 * k / (double)sh->D) : 0.0;
+  // 64 powers cost a few microseconds of a call's host time: keep the last table, by its base and D
+  static thread_local struct {
+    float base = 0.0f;
+    int D = 0;
+    double f[64];
+  } freq;
+  if (freq.base != sh->rope_base || freq.D != sh->D) {
+    for (int k = 0; k < 64; ++k)
+      freq.f[k] = k < sh->D / 2 ? std::pow((double)sh->rope_base, -2.0 * k / (double)sh->D) : 0.0;
+    freq.base = sh->rope_base;
+    freq.D = sh->D;
+  }
+  std::memcpy(sh->inv_freq, freq.f, sizeof(freq.f));
   return RTP_OK;
 }
 

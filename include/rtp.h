@@ -55,6 +55,7 @@ typedef enum rtp_status {
 #define RTP_DEV_SEQ_LEN  0x1  /* decode: seq_len[b] < 1 or > max_seq_len; sequence b skipped */
 #define RTP_DEV_POSITION 0x2  /* append/prefill: a position outside [0, max_ctx); rows skipped */
 #define RTP_DEV_TIMEOUT  0x4  /* decode or prefill: a bounded in-kernel wait gave up; that call's output is invalid */
+#define RTP_DEV_BLOCKS   0x8  /* paged cache: out of free blocks, or a block or slot outside the pool */
 
 typedef enum rtp_dtype { RTP_BF16 = 0, RTP_FP32 = 1 } rtp_dtype;
 
@@ -297,6 +298,169 @@ int rtp_prefill_attn(const rtp_layer_cfg* cfg, const rtp_cache* cache, const voi
                      uint32_t* sel_bitmask, float* sel_tau, int* sel_jcut, int* sel_count,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged 8-bit cache: K and V of many requests in one pool of blocks.
+ *
+ * A block holds block_size consecutive positions of one request, for every KV
+ * head, as e4m3 values with one fp32 scale per (block, KV head) for K and one
+ * for V: half the bytes of a bf16 cache.  Scales are powers of two, so a
+ * stored value times its scale is exact in bf16 and fp32, and a block whose
+ * scale grows keeps its values (only what falls below e4m3's smallest step is
+ * rounded again).  A request's blocks may lie anywhere in the pool; its row of
+ * the block table names them in order.  A step of a serving loop is
+ *     rtp_page_plan                       (once)
+ *     rtp_append_q8, rtp_attn_q8          (each layer)
+ * with the step's new tokens of all requests packed one after another:
+ * request b's tokens are rows [cu[b], cu[b + 1]) of every packed array.
+ *
+ * The layer is rtp_layer_cfg's: retrieval KV heads attend to the whole
+ * context, local ones to sinks and window.  There is no indexer on this cache
+ * and no ring: cfg->top_p must be 1, cfg->top_k and cfg->local_cap 0
+ * (RTP_ERR_SHAPE otherwise); cfg->idx_dim is not used.  cfg->max_ctx bounds a
+ * request's positions, and a row of the block table has
+ * ceil(max_ctx / block_size) entries.
+ */
+
+/* Pool of blocks (device memory owned by the caller).
+ *   k, v              [n_blocks][Hkv][block_size][D] e4m3
+ *   k_scale, v_scale  [n_blocks][Hkv] fp32, powers of two of at least 2^-64
+ *                     (smaller ones are read as 2^-64); the entries of a block
+ *                     that was never appended to are not read
+ *   status            one int of RTP_DEV_* bits, as in rtp_cache
+ *   n_blocks          n_blocks * Hkv * block_size < 2^31
+ *   block_size        16, 32, 64 or 128 positions
+ * rtp_append_q8 never stores a NaN in v (see there), and rtp_attn_q8 relies on
+ * that for rows below a request's length; other rows may hold anything.
+ */
+typedef struct rtp_q8_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int* status;
+  int n_blocks;
+  int block_size;
+} rtp_q8_cache;
+
+/* Rotary axes.  The rotary pair k (dims k and k + D/2) of a token turns by
+ * pos[axis[k]][token] * rope_base^(-2k/D): one axis for text, three (time,
+ * height, width) for pictures and video, the pairs shared out between them.
+ * A NULL rtp_rope_axes means one axis.  Positions are any int32. */
+typedef struct rtp_rope_axes {
+  int n_axes;             /* 1 .. 4 */
+  unsigned char axis[64]; /* of each pair k < D/2, below n_axes */
+} rtp_rope_axes;
+
+/* Host.  Bytes of each of k and v, and of each scale array. */
+int rtp_q8_cache_bytes(const rtp_layer_cfg* cfg, int n_blocks, int block_size, size_t* kv_bytes,
+                       size_t* scale_bytes);
+
+/* Block tables and slot map of one step, from the requests' lengths.
+ *
+ * Request b holds ctx_len[b] cached positions in its first
+ * have = ceil(ctx_len[b] / block_size) table entries.
+ *   new_len[b] >= 0: it brings that many tokens.  It takes the
+ *     need = ceil((ctx_len[b] + new_len[b]) / block_size) - have blocks that
+ *     they lack from the top of the stack of free blocks, in request order:
+ *     table entry have + i is free_list[top - 1 - before[b] - i], before[b]
+ *     the need of the requests ahead of it.  seq_len[b] = ctx_len[b] +
+ *     new_len[b].
+ *   new_len[b] < 0: it has ended.  Its blocks go on top of the stack, in table
+ *     order, before any is taken; seq_len[b] = 0.  Its table row stays as it
+ *     is and means nothing any more.
+ * `top` is n_free plus the blocks of ended requests.  Requests must not share
+ * blocks.
+ *
+ * A request that cannot be served is refused: it takes no block, seq_len[b] =
+ * ctx_len[b], its tokens get slot -1 (so rtp_append_q8 skips them), the others
+ * are served as if it were there.  That is where before[b] + need > top
+ * (RTP_DEV_BLOCKS), ctx_len[b] + new_len[b] > max_ctx or
+ * its packed tokens pass max_tokens (RTP_DEV_POSITION).  ctx_len[b] outside [0, max_ctx]
+ * counts as 0 cached and no new tokens (RTP_DEV_SEQ_LEN).
+ *
+ *   ctx_len, new_len  [B] int32, device
+ *   block_table       [B][ceil(max_ctx / block_size)] int32, device, in/out
+ *   free_list         [free_cap] int32, device, in/out: entries [0, n_free) are the stack
+ *   n_free            one int32, device, in [0, free_cap]
+ *   seq_len           [B] int32, device, out; may be ctx_len
+ *   cu_new            [B + 1] int32, device, out: first packed row of each request, then their number
+ *   slot_map          [max_tokens] int64, device, out: block * block_size + offset of each packed
+ *                     token; -1 for refused ones and for rows past the last token
+ *   positions         [max_tokens] int32, device, out: position of each packed token (0 past the last)
+ *   n_free_out        one int32, device, out; may be n_free
+ * A block number below 0 met in the table or the stack gives its tokens slot -1, and a
+ * block that the stack has no room for is dropped (both RTP_DEV_BLOCKS).
+ * cfg gives batch (at most 4096 here) and max_ctx. */
+int rtp_page_plan(const rtp_layer_cfg* cfg, int block_size, const int* ctx_len, const int* new_len,
+                  int* block_table, int* free_list, int free_cap, const int* n_free, int* seq_len,
+                  int* cu_new, int64_t* slot_map, int* positions, int max_tokens, int* n_free_out,
+                  int* status, void* stream);
+
+/* Append packed tokens to the pool.
+ *
+ * For packed token t with slot_map[t] = block * block_size + o >= 0, KV head h:
+ *   k row (block, h, o) = e4m3(RoPE(k_pre[t][h], pos[.][t]) / k_scale[block][h])
+ *   v row (block, h, o) = e4m3(v_in[t][h] / v_scale[block][h])
+ * to nearest, ties to even, from the rotation in 64 bits (one rounding).  The
+ * scale of a (block, head) becomes the least power of two, at least 2^-64, with
+ * |x| <= 448 scale for every value this call stores there, and not below its
+ * former one if the block held rows before (o > 0 for the call's first token
+ * in it); where it grows, those rows are rounded again to the new scale.
+ * A (token, head) row with a value that is not finite (in K, as rotated, or V) is stored
+ * as K all NaN and V all 0 and does not count for the scales: queries that see
+ * it answer NaN, no other query is touched.
+ *
+ *   k_pre, v_in  [n_tokens][Hkv][D] dtype, device; token t's [Hkv][D] slice
+ *                starts at element t * k_stride (v_stride) and is dense, so the
+ *                fused projection's output can be passed as it is.  Strides are
+ *                multiples of 16 bytes, at least Hkv * D; 0 means Hkv * D
+ *   slot_map     [n_tokens] int64, device; negative: the token is skipped
+ *   pos          [n_axes][n_tokens] int32, device
+ *   rope         host, or NULL for one axis
+ * Tokens of one block have to be consecutive, in ascending slots (as
+ * rtp_page_plan gives them): a block named by two separate runs, or a slot
+ * named twice, ends up with unspecified values.  Slots past the pool are
+ * skipped (RTP_DEV_BLOCKS). */
+int rtp_append_q8(const rtp_layer_cfg* cfg, const rtp_q8_cache* cache, const void* k_pre,
+                  int64_t k_stride, const void* v_in, int64_t v_stride, const int64_t* slot_map,
+                  const int* pos, const rtp_rope_axes* rope, int n_tokens, void* stream);
+
+/* Host.  Scratch bytes of rtp_attn_q8 for calls of up to n_tokens packed
+ * queries, max_q of one request and max_seq_len positions (0: cfg->max_ctx). */
+int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_tokens, int max_q,
+                                int max_seq_len, size_t* bytes);
+
+/* Attention of packed queries over the paged cache.
+ *
+ * Request b's n = cu_q[b + 1] - cu_q[b] queries are the last n of its
+ * seq_len[b] cached positions: query row t sits at i = seq_len[b] - n + t and
+ * sees positions [0, i]; local KV heads see of them the sinks [0, S) and the
+ * window [i - W + 1, i].
+ *   out = softmax(RoPE(q, pos) . k_j / sqrt(D)) v_j    k_j, v_j as stored, times their scales
+ * One token a request (decode), a few, or chunks, in any mix.  Arithmetic is
+ * on tensor cores with fp32 accumulation; queries and softmax weights enter
+ * them as fp16 (max_q * G <= 8, and always for fp32 layers: as two fp16 parts).
+ *
+ *   q_pre        [n_tokens][Hq][D] dtype, device, pre-RoPE; rows q_stride
+ *                elements apart (multiple of 16 bytes, at least Hq * D; 0 means Hq * D)
+ *   cu_q         [B + 1] int32, device, ascending from 0; rows from cu_q[B] on are left as they were in `out`
+ *   seq_len      [B] int32, device
+ *   block_table  [B][ceil(max_ctx / block_size)] int32, device
+ *   pos          [n_axes][n_tokens] int32, device
+ *   max_q        host: bound on a request's queries
+ *   max_seq_len  host: bound on seq_len (0: cfg->max_ctx)
+ *   out          [n_tokens][Hq][D] dtype, device, dense
+ *   workspace    >= rtp_attn_q8_workspace_bytes, 256-byte aligned, device; needs
+ *                no initialisation, clobbered; calls that may overlap need one each
+ * A request with seq_len[b] < n, or above max_seq_len, is skipped, its rows left as
+ * they were (RTP_DEV_SEQ_LEN); so is one with n < 0, n > max_q or rows past
+ * n_tokens (RTP_DEV_POSITION).  Positions whose block number lies outside the pool
+ * count as not there (RTP_DEV_BLOCKS); a query that sees none gets 0. */
+int rtp_attn_q8(const rtp_layer_cfg* cfg, const rtp_q8_cache* cache, const void* q_pre,
+                int64_t q_stride, const int* cu_q, const int* seq_len, const int* block_table,
+                const int* pos, const rtp_rope_axes* rope, int n_tokens, int max_q, int max_seq_len,
+                void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Kernel stages, for rtp_trace_stage. */
 typedef enum rtp_stage {
   RTP_STAGE_APPEND = 0,         /* rtp_append_kv: RoPE + cache + indexer-key store */
@@ -305,7 +469,10 @@ typedef enum rtp_stage {
   RTP_STAGE_DECODE_LOCAL = 3,   /* decode: sink/window attention of every KV head (beside the selection), final merge */
   RTP_STAGE_PREFILL_INDEX = 4,  /* prefill: per-row exact top-p selection */
   RTP_STAGE_PREFILL_ATTN = 5,   /* prefill: masked causal attention */
-  RTP_STAGE_COUNT = 6
+  RTP_STAGE_PAGE_PLAN = 6,      /* rtp_page_plan */
+  RTP_STAGE_APPEND_Q8 = 7,      /* rtp_append_q8 */
+  RTP_STAGE_ATTN_Q8 = 8,        /* rtp_attn_q8 (all of its kernels) */
+  RTP_STAGE_COUNT = 9
 } rtp_stage;
 
 /* Host.  Optional instrumentation (no work is skipped or added).  Arms a
