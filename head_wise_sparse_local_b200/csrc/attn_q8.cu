@@ -31,7 +31,7 @@
 // 23 B a clock, so 1400 clocks; the products are 192 mma.sync of 2 clocks each and 512
 // conversions of about 1 clock.  (tcgen05 would spend as long: its 128-row operand would be
 // 8 or 16 rows full.)
-#include "q8.cuh"
+#include "attn_q8.cuh"
 #include "tensor_map.h"
 
 namespace rtp {
@@ -42,22 +42,6 @@ constexpr int kAqThreads = kAqWarps * 32;
 constexpr int kAqTile = 32;   // positions a tile
 constexpr int kAqStages = 3;  // tiles in flight a warp
 constexpr int kAqCtasPerSm = 2;
-constexpr float kAqRescale = 8.f;  // M moves when a tile exceeds it by 2^8
-constexpr float kAqLift = 6.f;     // weights are held 2^6 up (at most 2^14 in fp16), away from fp16's small end
-
-struct __align__(64) AttnQ8Args {
-  CUtensorMap tm_k, tm_v;  // the pool as [n_blocks Hkv block_size][D] bytes, boxes of min(32, block_size) rows
-  Q8Pool pool;
-  RopeAxes rope;
-  int B, Hq, Hkv, G, S, W, rows, n_cta;
-  long long n_slots;  // partials that the workspace holds
-  uint64_t ret_mask;
-  AttnQ8Call c;
-  float* part;  // [n_cta + items][rows][D] O, then [..][rows][2] (M, l)
-  float* part_ml;
-  unsigned long long wait_ns;
-  double inv_freq[64];
-};
 
 // A request's queries and tiles.
 struct ReqQ8 {
@@ -72,21 +56,13 @@ struct ReqQ8 {
 
 __device__ __forceinline__ ReqQ8 load_req(const AttnQ8Args& a, int b, int& flags) {
   ReqQ8 r = {};
-  const int q0 = a.c.cu_q[b], q1 = a.c.cu_q[b + 1], L = a.c.seq_len[b];
-  const long long n = (long long)q1 - q0;
-  if (n < 0 || n > a.c.max_q || q0 < 0 || q1 > a.c.n_tokens) {
-    flags |= RTP_DEV_POSITION;
-    return r;
-  }
-  if (n == 0) return r;
-  if (L < n || L > a.c.max_seq_len) {
-    flags |= RTP_DEV_SEQ_LEN;
-    return r;
-  }
-  r.q0 = q0;
-  r.n = (int)n;
+  const ReqRows x = load_rows(a, b, flags);
+  if (x.n == 0 || (long long)x.n * a.G > a.small_rows) return r;
+  const int L = x.L;
+  r.q0 = x.q0;
+  r.n = x.n;
   r.L = L;
-  r.rc = (int)((n * a.G + a.rows - 1) / a.rows);
+  r.rc = (x.n * a.G + a.rows - 1) / a.rows;
   r.tr = (L - 1) / kAqTile + 1;
   r.ns = min((a.S + kAqTile - 1) / kAqTile, r.tr);
   r.w0 = max(0, L - r.n - a.W + 1) / kAqTile;
@@ -150,17 +126,6 @@ __device__ __forceinline__ void ldsm_b8_t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-  return e;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // What a tile's consumers need beside its rows; the scales arrive by cp.async.
 struct __align__(16) TileMeta {
   float ks[2], vs[2];  // scales of its first and second 16 positions
@@ -178,12 +143,6 @@ struct AqSmem {
   static constexpr int kMPitch = D + 2;                                // joining the warps: O rows, M, l (over the ring)
   static_assert(kAqWarps * ROWS * kMPitch * 4 <= kRing, "the warps' partials fit in the ring");
 };
-
-// out = O / l of one row element.
-template <typename T>
-__device__ __forceinline__ T finish(float o, float l) {
-  return from_f32<T>(l == 0.f ? 0.f : o / l);  // l = 0: no position of the row is there
-}
 
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const __grid_constant__ AttnQ8Args a) {
@@ -352,10 +311,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
       float m = 0.f;
       for (int k = lane; k < D; k += 32) m = fmaxf(m, fabsf(s_q[r * SM::kQPitch + k]));
       m = warp_max(m);
-      // row scale 2^e with |q| 2^-e < 2^9: the low part keeps 11 more bits above fp16's smallest step
-      int e = (int)(__float_as_uint(m) >> 23) - 127 - 8;
-      e = m == 0.f ? 0 : min(max(e, -100), 110);
-      if (lane == 0) s_qs[r] = __uint_as_float((uint32_t)(e + 127) << 23);
+      if (lane == 0) s_qs[r] = query_scale(m);
     }
     __syncthreads();
     uint32_t qa[KS][4];
@@ -675,15 +631,35 @@ __global__ void __launch_bounds__(D) attn_q8_join_kernel(const __grid_constant__
   static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + threadIdx.x] = finish<T>(os, ls);
 }
 
-// Query rows of an item: 8 (queries in two fp16 parts) for fp32 layers and
-// where a KV head's rows fit in 8, else 16.
-int item_rows(const Shape& sh, int max_q) { return sh.dtype == RTP_FP32 || (long long)max_q * sh.G <= 8 ? 8 : 16; }
+// Requests of up to this many query rows a KV head (n G) are streamed, larger
+// ones of bf16 layers are chunks.  Streaming reads the cache once for each 16
+// rows; a chunk's 128-row products cost the same for any number up to 128.
+constexpr int kAqSmallRows = 32;
 
-long long max_items(const Shape& sh, int n_tokens, int max_q, int rows) {
+// All requests streamed, all chunks, or (by their rows, on the device) some of each.
+int small_rows(const Shape& sh, int max_q) {
+  if (sh.dtype == RTP_FP32 || (long long)max_q * sh.G <= kAqSmallRows) return INT32_MAX;
+  return sh.B == 1 ? 0 : kAqSmallRows;
+}
+
+// Queries that a streamed request can have.
+int small_q(const Shape& sh, int max_q) {
+  const int s = small_rows(sh, max_q);
+  return s == INT32_MAX ? max_q : s / sh.G;
+}
+
+// Query rows of a streamed item: 8 (queries in two fp16 parts) for fp32 layers
+// and where a KV head's rows fit in 8, else 16.
+int item_rows(const Shape& sh, int max_q) {
+  return sh.dtype == RTP_FP32 || (long long)small_q(sh, max_q) * sh.G <= 8 ? 8 : 16;
+}
+
+long long max_items(const Shape& sh, int n_tokens, int max_q) {
   // sum over requests of ceil(n G / rows)
+  const int rows = item_rows(sh, max_q), q = small_q(sh, max_q);
   const long long reqs = sh.B < n_tokens ? sh.B : n_tokens;
   const long long by_tokens = (long long)n_tokens * sh.G / rows + reqs;
-  const long long by_max = reqs * (((long long)max_q * sh.G + rows - 1) / rows);
+  const long long by_max = reqs * (((long long)q * sh.G + rows - 1) / rows);
   return sh.Hkv * (by_tokens < by_max ? by_tokens : by_max);
 }
 
@@ -712,13 +688,20 @@ cudaError_t launch(const AttnQ8Args& a, long long items, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_q8_workspace_bytes(const Shape& sh, int log_bs, int n_tokens, int max_q, int max_seq_len) {
-  (void)log_bs;
-  (void)max_seq_len;
-  const int rows = item_rows(sh, max_q);
-  const size_t slots = (size_t)kAqMaxCtas + (size_t)max_items(sh, n_tokens, max_q, rows);
-  const size_t bytes = slots * rows * (sh.D + 2) * sizeof(float);
+namespace {
+size_t stream_workspace_bytes(const Shape& sh, int n_tokens, int max_q) {
+  if (small_rows(sh, max_q) == 0) return 0;
+  const size_t slots = (size_t)kAqMaxCtas + (size_t)max_items(sh, n_tokens, max_q);
+  const size_t bytes = slots * item_rows(sh, max_q) * (sh.D + 2) * sizeof(float);
   return (bytes + 255) / 256 * 256;
+}
+}  // namespace
+
+size_t attn_q8_workspace_bytes(const Shape& sh, int n_tokens, int max_q) {
+  size_t bytes = stream_workspace_bytes(sh, n_tokens, max_q);
+  const int small = small_rows(sh, max_q);
+  if (small != INT32_MAX) bytes += chunk_workspace_bytes(sh, n_tokens, max_q, small);
+  return bytes < 256 ? 256 : bytes;
 }
 
 int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, const AttnQ8Call& c, void* ws,
@@ -744,19 +727,27 @@ int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, co
   a.rows = item_rows(sh, c.max_q);
   a.wait_ns = 400ull * 1000 * 1000;
   for (int i = 0; i < 64; ++i) a.inv_freq[i] = sh.inv_freq[i];
-  const long long items = max_items(sh, c.n_tokens, c.max_q, a.rows);
+  a.small_rows = small_rows(sh, c.max_q);
+  const long long items = max_items(sh, c.n_tokens, c.max_q);
   a.n_cta = kAqMaxCtas;
   a.part = static_cast<float*>(ws);
   a.n_slots = kAqMaxCtas + items;
   a.part_ml = a.part + (size_t)a.n_slots * a.rows * sh.D;
-  cudaError_t e;
+  const bool chunks = a.small_rows != INT32_MAX;
+  if (chunks)
+    chunk_carve(sh, c.n_tokens, c.max_q, a.small_rows,
+                static_cast<unsigned char*>(ws) + stream_workspace_bytes(sh, c.n_tokens, c.max_q), &a);
+  cudaError_t e = cudaSuccess;
   trace_begin(RTP_STAGE_ATTN_Q8, st);
-  if (sh.dtype == RTP_BF16) {
-    if (a.rows == 8) e = sh.D == 128 ? launch<__nv_bfloat16, 128, 8>(a, items, st) : launch<__nv_bfloat16, 64, 8>(a, items, st);
-    else e = sh.D == 128 ? launch<__nv_bfloat16, 128, 16>(a, items, st) : launch<__nv_bfloat16, 64, 16>(a, items, st);
-  } else {
-    e = sh.D == 128 ? launch<float, 128, 8>(a, items, st) : launch<float, 64, 8>(a, items, st);
+  if (a.small_rows > 0) {
+    if (sh.dtype == RTP_BF16) {
+      if (a.rows == 8) e = sh.D == 128 ? launch<__nv_bfloat16, 128, 8>(a, items, st) : launch<__nv_bfloat16, 64, 8>(a, items, st);
+      else e = sh.D == 128 ? launch<__nv_bfloat16, 128, 16>(a, items, st) : launch<__nv_bfloat16, 64, 16>(a, items, st);
+    } else {
+      e = sh.D == 128 ? launch<float, 128, 8>(a, items, st) : launch<float, 64, 8>(a, items, st);
+    }
   }
+  if (chunks && e == cudaSuccess) e = launch_attn_q8_chunks(sh, a, st);
   trace_end(RTP_STAGE_ATTN_Q8, st);
   if (e != cudaSuccess) {
     cudaGetLastError();

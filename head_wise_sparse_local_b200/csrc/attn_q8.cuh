@@ -1,0 +1,94 @@
+// What the two attention kernels of the paged 8-bit cache share: the streaming
+// kernel (attn_q8.cu) and the chunk kernel (attn_q8_tc.cu).
+#pragma once
+
+#include <cuda.h>  // CUtensorMap
+
+#include "q8.cuh"
+
+namespace rtp {
+
+constexpr float kAqRescale = 8.f;  // the running maximum moves when a tile exceeds it by 2^8
+constexpr float kAqLift = 6.f;     // weights are held 2^6 up (at most 2^14 in fp16), away from fp16's small end
+
+// 256 query rows of one (request, KV head).
+struct ChunkItem {
+  int b, h, grp, tiles;
+};
+
+struct __align__(64) AttnQ8Args {
+  CUtensorMap tm_k, tm_v;  // the pool as [n_blocks Hkv block_size][D] bytes, boxes of min(32, block_size) rows
+  Q8Pool pool;
+  RopeAxes rope;
+  int B, Hq, Hkv, G, S, W, rows, n_cta;
+  int small_rows;     // requests of more query rows (n G) a KV head go to the chunk kernel
+  long long n_slots;  // partials that the workspace holds
+  uint64_t ret_mask;
+  AttnQ8Call c;
+  float* part;  // [n_cta + items][rows][D] O, then [..][rows][2] (M, l)
+  float* part_ml;
+  unsigned long long wait_ns;
+  double inv_freq[64];
+  // the chunk kernel's share of the workspace
+  struct ChunkItem* items;
+  long long* prefix;  // tiles ahead of each item, then their number
+  int* req_items;     // [B + 1] items ahead of each request
+  float* cpart;       // partials of cut items: [2 CTAs][256][D], and (M, l)
+  float* cpart_ml;
+  int max_chunk_items;
+};
+
+
+// First packed row, number of queries and cached positions of request b;
+// n = 0 where it has nothing to do or is refused (`flags`).
+struct ReqRows {
+  int q0, n, L;
+};
+
+__device__ __forceinline__ ReqRows load_rows(const AttnQ8Args& a, int b, int& flags) {
+  const int q0 = a.c.cu_q[b], q1 = a.c.cu_q[b + 1], L = a.c.seq_len[b];
+  const long long n = (long long)q1 - q0;
+  if (n < 0 || n > a.c.max_q || q0 < 0 || q1 > a.c.n_tokens) {
+    flags |= RTP_DEV_POSITION;
+    return ReqRows{0, 0, 0};
+  }
+  if (n == 0) return ReqRows{0, 0, 0};
+  if (L < n || L > a.c.max_seq_len) {
+    flags |= RTP_DEV_SEQ_LEN;
+    return ReqRows{0, 0, 0};
+  }
+  return ReqRows{q0, (int)n, L};
+}
+
+// Factor 2^e that brings a query row's largest magnitude m into [2^8, 2^9), so
+// that neither fp16's largest value nor its smallest step is in the way.
+__device__ __forceinline__ float query_scale(float m) {
+  int e = (int)(__float_as_uint(m) >> 23) - 127 - 8;
+  e = m == 0.f ? 0 : min(max(e, -40), 110);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// out = O / l of one row element.
+template <typename T>
+__device__ __forceinline__ T finish(float o, float l) {
+  return from_f32<T>(l == 0.f ? 0.f : o / l);  // l = 0: no position of the row is there
+}
+
+// The chunk kernel (bf16 layers): workspace, and its launches for the requests
+// of more than a.small_rows query rows a KV head.
+size_t chunk_workspace_bytes(const Shape& sh, int n_tokens, int max_q, int small_rows);
+void chunk_carve(const Shape& sh, int n_tokens, int max_q, int small_rows, void* ws, AttnQ8Args* a);
+cudaError_t launch_attn_q8_chunks(const Shape& sh, const AttnQ8Args& a, cudaStream_t st);
+
+}  // namespace rtp

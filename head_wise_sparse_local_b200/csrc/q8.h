@@ -45,7 +45,7 @@ struct AttnQ8Call {
   int n_tokens, max_q, max_seq_len;
   void* out;
 };
-size_t attn_q8_workspace_bytes(const Shape& sh, int log_bs, int n_tokens, int max_q, int max_seq_len);
+size_t attn_q8_workspace_bytes(const Shape& sh, int n_tokens, int max_q);
 int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, const AttnQ8Call& c, void* ws,
                    cudaStream_t st);
 

@@ -147,7 +147,7 @@ int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_
   if (rc != RTP_OK) return rc;
   if (!bytes) return fail(RTP_ERR_INVALID, "bytes is NULL");
   if ((rc = attn_bounds(sh, n_tokens, max_q, &max_seq_len)) != RTP_OK) return rc;
-  *bytes = attn_q8_workspace_bytes(sh, log_bs, n_tokens, max_q, max_seq_len);
+  *bytes = attn_q8_workspace_bytes(sh, n_tokens, max_q);
   return RTP_OK;
 }
 
@@ -172,7 +172,7 @@ int rtp_attn_q8(const rtp_layer_cfg* cfg, const rtp_q8_cache* cache, const void*
   if (!workspace) return fail(RTP_ERR_WORKSPACE, "workspace is NULL");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(RTP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  if (workspace_bytes < attn_q8_workspace_bytes(sh, log_bs, n_tokens, max_q, max_seq_len))
+  if (workspace_bytes < attn_q8_workspace_bytes(sh, n_tokens, max_q))
     return fail(RTP_ERR_WORKSPACE, "workspace smaller than rtp_attn_q8_workspace_bytes");
   AttnQ8Call c;
   c.q_pre = q_pre; c.q_stride = q_stride; c.cu_q = cu_q; c.seq_len = seq_len; c.block_table = block_table;

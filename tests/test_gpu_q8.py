@@ -15,6 +15,8 @@ Z = max_j sum_d |q_d k_jd| / sqrt(D):
   - weights below fp16's smallest step, against the largest weight w of a value
     scaled by its block: L 2^-31 448 max_j (p_j vs_j) <= L 2^-22 max_j p_j max|v|;
   - the output's rounding, |o| eps / 2 (bf16 2^-8, fp32 2^-24).
+Chunks (more than 32 query rows a KV head) form a quarter of their weights by a
+cubic whose relative error is 7.5e-5 < 2^-13: A 2^-13, and twice that in e.
 """
 
 import math
@@ -393,7 +395,8 @@ class _Attn:
                         hq = h * self.G + g
                         o, A, Z = ref.attend(qr[self.cu[b] + t, hq], k, v, seen)
                         e = Z * (self.r_q() + 2.0 ** -20)
-                        bound = o.abs() * half + A * (math.expm1(2 * e) + r_w + (L / 16 + 64) * 2.0 ** -23) + L * 2.0 ** -22 * vmax * min(1.0, 64.0 / max(1, int(seen.sum()))) + 1e-30
+                        r_p = 2.0 ** -12 if self.dtype == "bf16" and self.max_q * self.G > 32 else 0.0
+                        bound = o.abs() * half + A * (math.expm1(2 * e) + r_p + r_w + (L / 16 + 64) * 2.0 ** -23) + L * 2.0 ** -22 * vmax * min(1.0, 64.0 / max(1, int(seen.sum()))) + 1e-30
                         err = (got[self.cu[b] + t, hq] - o).abs()
                         ratio = float((err / bound).max())
                         worst = max(worst, ratio)
@@ -426,6 +429,100 @@ def test_a_few_queries_a_request(dtype, G, new, bs):
     """Drafts: every query has its own causal border, window and position."""
     a = _Attn([400, 90, 66, 1300], new, G=G, bs=bs, dtype=dtype, S=10, W=50, sections=AXIS3[128], seed=G)
     a.check(a.run())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,new", [(1, [33, 257, 128]), (2, [300, 17, 64]), (4, [9, 64, 65]), (8, [5, 33, 100])])
+@pytest.mark.parametrize("bs", [16, 64, 128])
+def test_chunks(D, G, new, bs):
+    """Rows that end inside a slot, a group and a tile; contexts before the chunk."""
+    a = _Attn([max(33, new[0]), 700, 390], new, D=D, G=G, bs=bs, S=10, W=150, sections=AXIS3[D], seed=D + G + bs)
+    got = a.run()
+    a.check(got, rows={(b, t) for b, n in enumerate(new) for t in range(n) if t % 7 == 0 or t >= n - 2})
+    assert int(a.status) == 0
+
+
+@pytest.mark.parametrize("S,W,ret", [(0, 1, ()), (0, 1, (0, 1)), (129, 300, (1,)), (64, 128, ()), (2000, 1, ())])
+def test_chunk_masks(S, W, ret):
+    a = _Attn([1500], [600], G=2, bs=32, S=S, W=W, ret=ret, seed=S + W)
+    a.check(a.run(), rows={(0, t) for t in range(0, 600, 13)} | {(0, 599)})
+
+
+def test_chunks_beside_decoding_requests():
+    """Streamed and chunk requests, idle ones, and rows behind the last, in one call."""
+    new = [1, 200, 0, 8, 9, 1, 513, 2]
+    a = _Attn([900, 200, 50, 77, 300, 1, 1111, 640], new, G=4, bs=16, S=20, W=128, pad=7, seed=3)
+    got = a.run()
+    assert bool((got[sum(new):] == 77.0).all()) and int(a.status) == 0
+    a.check(got, rows={(b, t) for b, n in enumerate(new) for t in range(n) if t % 17 == 0 or t == n - 1})
+
+
+def test_chunk_long_context_is_split_and_joined():
+    a = _Attn([20000], [70], hkv=2, G=4, bs=64, S=64, W=2048, ret=(1,), seed=31)
+    a.check(a.run(), rows={(0, t) for t in range(0, 70, 9)} | {(0, 69)})
+    a = _Attn([9000], [3], hkv=1, G=8, bs=64, ret=(0,), seed=32, pad=40)  # one small request where max_q allows a chunk
+    a.device()
+    a.max_q = 40
+    n = rtp.rtp_attn_q8_workspace_bytes(a.cfg, a.bs, a.N, 40, 0)
+    a.ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    a.call()
+    torch.cuda.synchronize()
+    a.check(a.out.cpu().double())
+
+
+def test_chunk_that_is_its_whole_context():
+    a = _Attn([1000, 129], [1000, 129], G=1, hkv=2, bs=64, S=2, W=70, ret=(1,), seed=33)
+    a.check(a.run(), rows={(b, t) for b in range(2) for t in (0, 1, 2, 69, 70, 71, 127, 128)} | {(0, 999), (0, 500)})
+
+
+def test_chunk_blocks_outside_the_pool_and_stored_nans():
+    a = _Attn([400], [100], G=2, bs=64, W=64, S=0, ret=(0,), seed=34)
+    a.pool.k[a.table[0, 350 // 64], :, 350 % 64] = math.nan  # position 350: row 50 of the chunk
+    a.pool.v[a.table[0, 350 // 64], :, 350 % 64] = 0.0
+    a.device()
+    tab = a.dtab.clone()
+    tab[0, 1] = a.dk.shape[0] + 5
+    a.dtab.copy_(tab)
+    a.call()
+    torch.cuda.synchronize()
+    got = a.out.cpu().double()
+    assert int(a.status) == rtp.RTP_DEV_BLOCKS
+    assert bool(torch.isnan(got[50:]).all()) and bool(torch.isfinite(got[:50]).all())
+    a.pool.k.nan_to_num_(0.0)
+    a.check(got, rows={(0, t) for t in range(0, 50, 7)}, there=[torch.arange(400) // 64 != 1])
+
+
+def test_chunk_value_scales_far_apart_and_large_scores():
+    a = _Attn([512], [60], bs=64, hkv=1, G=4, ret=(0,), seed=35, q_scale=20.0)
+    e = torch.tensor([-30, -20, 0, 10, -7, -5, -60, -1], dtype=torch.float64)
+    for i in range(8):
+        a.pool.vs[a.table[0, i]] = 2.0 ** e[i]
+    a.pool.v[a.table[0, 3]] = 0.0
+    a.pool.vs[a.table[0, 3]] = ref.SCALE_MIN
+    a.check(a.run())
+
+
+def test_chunk_call_repeated_captured_and_on_two_streams():
+    a, b = _Attn([800, 60], [300, 1], seed=36).device(), _Attn([1300], [256], seed=37).device()
+    a.call()
+    torch.cuda.synchronize()
+    first = a.out.clone()
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            a.call()
+    a.ws.random_(0, 255)
+    a.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            g.replay()
+        b.call(stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(first, a.out)
+    a.check(a.out.cpu().double(), rows={(0, 0), (0, 150), (0, 299), (1, 0)})
+    b.check(b.out.cpu().double(), rows={(0, 0), (0, 77), (0, 255)})
 
 
 def test_first_tokens_of_a_request():
