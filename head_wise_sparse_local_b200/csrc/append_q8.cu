@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_q8_kernel(const __grid_
         uint32_t* w = reinterpret_cast<uint32_t*>(base);
         for (int i = sub * 32 + lane; i < off * (D / 4); i += wpr * 32) {
           const uint32_t u = w[i];
-          const uint32_t x = e4m3x2_to_f16x2(u), y = e4m3x2_to_f16x2(u >> 16);
+          uint32_t x, y;
+          e4m3x4_to_f16x4(u, x, y);
           const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&x));
           const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&y));
           w[i] = f32x2_to_e4m3x2(lo.x * f, lo.y * f) | (f32x2_to_e4m3x2(hi.x * f, hi.y * f) << 16);

@@ -42,6 +42,7 @@ constexpr int kAqThreads = kAqWarps * 32;
 constexpr int kAqTile = 32;   // positions a tile
 constexpr int kAqStages = 3;  // tiles in flight a warp
 constexpr int kAqCtasPerSm = 2;
+constexpr int kAqMaxCtas = 148 * kAqCtasPerSm;  // every SM of a B200
 
 // A request's queries and tiles.
 struct ReqQ8 {
@@ -49,9 +50,7 @@ struct ReqQ8 {
   int rc;         // row chunks
   int tr, tl;     // tiles of a retrieval and of a local KV head
   int ns, w0;     // a local head's tiles: [0, ns) and [w0, tr)
-  __device__ __forceinline__ long long tiles(int R, int Hkv) const {
-    return (long long)rc * ((long long)R * tr + (long long)(Hkv - R) * tl);
-  }
+  __device__ __forceinline__ uint32_t tiles(int R, int Hkv) const { return (uint32_t)rc * (uint32_t)(R * tr + (Hkv - R) * tl); }
 };
 
 __device__ __forceinline__ ReqQ8 load_req(const AttnQ8Args& a, int b, int& flags) {
@@ -75,31 +74,74 @@ __device__ __forceinline__ ReqQ8 load_req(const AttnQ8Args& a, int b, int& flags
   return r;
 }
 
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Tiles a CTA takes: an equal share of the line, at least one a warp.
+__device__ __forceinline__ uint32_t share_of(uint32_t total) {
+  return max((total + kAqMaxCtas - 1) / kAqMaxCtas, (uint32_t)kAqWarps);
 }
-__device__ __forceinline__ long long warp_scan_ll(long long v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long n = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += n;
+
+// Where position `part` * share of the line lies (every warp for itself): its
+// request, and the tiles and items ahead of that.  b < 0: past the end.
+struct LineAt {
+  int b;
+  uint32_t at, share, total, tiles, items;
+};
+
+__device__ __forceinline__ LineAt locate(const AttnQ8Args& a, uint32_t part, int& flags) {
+  const int lane = threadIdx.x & 31, R = __popcll(a.ret_mask);
+  LineAt p = {-1, 0u, 0u, 0u, 0u, 0u};
+  auto sums = [&](int b0, uint32_t& t, uint32_t& it, uint32_t& ts, uint32_t& is) {
+    ReqQ8 r = {};
+    if (b0 + lane < a.B) r = load_req(a, b0 + lane, flags);
+    t = r.tiles(R, a.Hkv);
+    it = (uint32_t)(r.rc * a.Hkv);
+    ts = warp_incl_scan_u32(t);
+    is = warp_incl_scan_u32(it);
+  };
+  uint32_t t, it, ts, is;
+  sums(0, t, it, ts, is);
+  p.total = __shfl_sync(0xffffffffu, ts, 31);
+  for (int b0 = 32; b0 < a.B; b0 += 32) {
+    uint32_t t2, it2, ts2, is2;
+    sums(b0, t2, it2, ts2, is2);
+    p.total += __shfl_sync(0xffffffffu, ts2, 31);
   }
-  return v;
+  p.share = share_of(p.total);
+  p.at = part * p.share;
+  if (p.at >= p.total) return p;
+  for (int b0 = 0;;) {
+    const unsigned m = __ballot_sync(0xffffffffu, p.tiles + ts > p.at);
+    if (m) {
+      const int l = __ffs(m) - 1;
+      p.b = b0 + l;
+      p.tiles += __shfl_sync(0xffffffffu, ts - t, l);
+      p.items += __shfl_sync(0xffffffffu, is - it, l);
+      return p;
+    }
+    p.tiles += __shfl_sync(0xffffffffu, ts, 31);
+    p.items += __shfl_sync(0xffffffffu, is, 31);
+    b0 += 32;
+    sums(b0, t, it, ts, is);
+  }
 }
 
-// All tiles of the call (every warp for itself).
-__device__ __forceinline__ long long total_tiles(const AttnQ8Args& a, int R, int& flags) {
-  long long t = 0;
-  for (int b = threadIdx.x & 31; b < a.B; b += 32) t += load_req(a, b, flags).tiles(R, a.Hkv);
-  return warp_sum_ll(t);
-}
-
-// Tiles a CTA takes: an equal share, at least one a warp.
-__device__ __forceinline__ long long share_of(const AttnQ8Args& a, long long total) {
-  return max((total + a.n_cta - 1) / a.n_cta, (long long)kAqWarps);
+// The item at `rel` tiles into a request: its KV head and row chunk; `rel`
+// becomes the tile's number in it.
+struct ItemAt {
+  int h, rch, nt;  // nt: its tiles
+};
+__device__ __forceinline__ ItemAt item_at(const AttnQ8Args& a, const ReqQ8& r, uint32_t& rel) {
+  ItemAt x = {0, 0, 0};
+  for (;; ++x.h) {
+    x.nt = (a.ret_mask >> x.h) & 1ull ? r.tr : r.tl;
+    const uint32_t all = (uint32_t)(x.nt * r.rc);
+    if (rel < all) break;
+    rel -= all;
+  }
+  if (r.rc > 1) {
+    x.rch = (int)(rel / (uint32_t)x.nt);
+    rel -= (uint32_t)x.rch * (uint32_t)x.nt;
+  }
+  return x;
 }
 
 __device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* tm, int y, uint64_t* bar, uint64_t pol) {
@@ -175,32 +217,13 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
 
   const int R = __popcll(a.ret_mask);
   int flags = 0;
-  const long long total = total_tiles(a, R, flags);
+  LineAt line = locate(a, blockIdx.x, flags);
   if (blockIdx.x == 0 && warp == 0 && flags) atomicOr(a.pool.status, flags);
-  const long long share = share_of(a, total);
-  long long at = (long long)blockIdx.x * share;
-  const long long end = min(total, at + share);
-  if (at >= end) return;  // uniform
-  // ---- the request that holds tile `at`: tiles and items ahead of it ----
-  int b = 0;
-  long long b_tiles = 0, b_items = 0;
-  for (int b0 = 0;; b0 += 32) {
-    int dummy = 0;
-    ReqQ8 r = {};
-    if (b0 + lane < a.B) r = load_req(a, b0 + lane, dummy);
-    const long long t = r.tiles(R, a.Hkv), it = (long long)r.rc * a.Hkv;
-    const long long ts = warp_scan_ll(t), is = warp_scan_ll(it);
-    const unsigned m = __ballot_sync(0xffffffffu, b_tiles + ts > at);
-    if (m) {
-      const int l = __ffs(m) - 1;
-      b = b0 + l;
-      b_tiles += __shfl_sync(0xffffffffu, ts - t, l);
-      b_items += __shfl_sync(0xffffffffu, is - it, l);
-      break;
-    }
-    b_tiles += __shfl_sync(0xffffffffu, ts, 31);
-    b_items += __shfl_sync(0xffffffffu, is, 31);
-  }
+  flags = 0;
+  if (line.b < 0) return;  // uniform
+  uint32_t at = line.at;
+  const uint32_t end = min(line.total, at + line.share);
+  int b = line.b;
 
   const uint64_t pol = l2_evict_first();
   const int bs1 = (1 << a.pool.log_bs) - 1;
@@ -211,29 +234,22 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
 
   while (at < end) {
     // ---- the segment: tiles [u0, u1) of item (b, h, rch) ----
-    long long rel = at - b_tiles;
+    uint32_t rel = at - line.tiles;
     while (rel >= rq.tiles(R, a.Hkv)) {  // on to the next request that has tiles
-      b_tiles += rq.tiles(R, a.Hkv);
-      b_items += (long long)rq.rc * a.Hkv;
-      rel = at - b_tiles;
+      line.tiles += rq.tiles(R, a.Hkv);
+      line.items += (uint32_t)(rq.rc * a.Hkv);
+      rel = at - line.tiles;
       rq = load_req(a, ++b, flags);
     }
-    int h = 0;
-    bool ret = a.ret_mask & 1ull;
-    int nt = ret ? rq.tr : rq.tl;
-    while (rel >= (long long)nt * rq.rc) {
-      rel -= (long long)nt * rq.rc;
-      ++h;
-      ret = (a.ret_mask >> h) & 1ull;
-      nt = ret ? rq.tr : rq.tl;
-    }
-    const int rch = (int)(rel / nt);
-    const int u0 = (int)(rel - (long long)rch * nt);
-    const int u1 = (int)min((long long)nt, u0 + (end - at));
-    const long long item = b_items + (long long)h * rq.rc + rch;
+    const ItemAt x = item_at(a, rq, rel);
+    const int h = x.h, rch = x.rch, nt = x.nt;
+    const bool ret = (a.ret_mask >> h) & 1ull;
+    const int u0 = (int)rel;
+    const int u1 = (int)min((uint32_t)nt, rel + (end - at));
+    const uint32_t item = line.items + (uint32_t)(h * rq.rc + rch);
     const int row0 = rch * ROWS, n_rows = min(ROWS, rq.n * a.G - row0);
     const int i0 = rq.L - rq.n;                            // position of the request's first query
-    const int i_lo = i0 + row0 / a.G, i_hi = i0 + (row0 + n_rows - 1) / a.G;  // of this chunk's rows
+    const int i_lo = i0 + (row0 >> a.log_g), i_hi = i0 + ((row0 + n_rows - 1) >> a.log_g);  // of this chunk's rows
     const int* tab = a.c.block_table + (size_t)b * a.pool.table_cols;
     const int mine = u0 + warp < u1 ? (u1 - u0 - warp + kAqWarps - 1) / kAqWarps : 0;  // this warp's tiles
 
@@ -248,7 +264,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
       id[0] = tab[c0];
       id[1] = split ? (j0 + 16 < rq.L ? tab[c0 + 1] : -1) : id[0];
     };
-    auto issue = [&](int n, int s, const int (&id)[2]) {  // lane 0: tile n into ring stage s
+    auto issue = [&](int n, int s, const int (&id)[2]) {  // one lane: tile n into ring stage s
       const int j0 = tile_key(n);
       int there = 0, y[2], blk[2];
 #pragma unroll
@@ -275,37 +291,41 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
       tma_tile(dst + kAqTile * D, &a.tm_v, y[0], &bar[s], pol);
       if (split) tma_tile(dst + kAqTile * D + 16 * D, &a.tm_v, y[1], &bar[s], pol);
     };
-    int next_id[2] = {0, 0};  // blocks of the next tile to issue
-    if (lane == 0) {
-      int s = st;
-#pragma unroll
-      for (int n = 0; n < kAqStages; ++n) {
-        if (n < mine) {
-          int id[2];
-          block_ids(n, id);
-          issue(n, s, id);
-        }
-        s = s + 1 == kAqStages ? 0 : s + 1;
-      }
-      if (mine > kAqStages) block_ids(kAqStages, next_id);
+    // the first tiles, a lane each, so that their block numbers are read at once
+    if (lane < kAqStages && lane < mine) {
+      int id[2], s = st + lane;
+      block_ids(lane, id);
+      issue(lane, s >= kAqStages ? s - kAqStages : s, id);
     }
+    int next_id[2] = {0, 0};  // blocks of the next tile to issue
+    if (lane == 0 && mine > kAqStages) block_ids(kAqStages, next_id);
 
     // ---- queries: rotated in fp32, then as fp16 operands of a power-of-two scale a row ----
-    for (int task = tid; task < ROWS * (D / 2); task += kAqThreads) {
-      const int r = task / (D / 2), k = task % (D / 2);
-      float y1 = 0.f, y2 = 0.f;
-      if (r < n_rows) {
-        const int tok = rq.q0 + (row0 + r) / a.G, hq = h * a.G + (row0 + r) % a.G;
-        const T* q = static_cast<const T*>(a.c.q_pre) + (size_t)tok * a.c.q_stride + (size_t)hq * D;
-        const float x1 = to_f32(q[k]), x2 = to_f32(q[k + D / 2]);
-        float c, s;
-        rope_cos_sin(a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + tok], a.inv_freq[k], c, s);
-        y1 = x1 * c - x2 * s;
-        y2 = x2 * c + x1 * s;
-      }
-      s_q[r * SM::kQPitch + k] = y1;
-      s_q[r * SM::kQPitch + k + D / 2] = y2;
+    // (a thread turns a rotary pair of all the chunk's rows of one token)
+    const int tok0 = row0 >> a.log_g, n_tok = ((row0 + n_rows - 1) >> a.log_g) - tok0 + 1;
+    for (int task = tid; task < n_tok * (D / 2); task += kAqThreads) {
+      const int tl = task / (D / 2), k = task % (D / 2), tok = rq.q0 + tok0 + tl;
+      const int p = a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + tok];
+      const int ra = max(((tok0 + tl) << a.log_g) - row0, 0), rb = min(((tok0 + tl + 1) << a.log_g) - row0, n_rows);
+      const T* q = static_cast<const T*>(a.c.q_pre) + (size_t)tok * a.c.q_stride +
+                   (size_t)(h * a.G + ((row0 + ra) & (a.G - 1))) * D + k;
+      float x1[8], x2[8];  // a token has at most 8 rows
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (ra + r < rb) {
+          x1[r] = to_f32(q[(size_t)r * D]);
+          x2[r] = to_f32(q[(size_t)r * D + D / 2]);
+        }
+      float c, s;
+      rope_turns(p, a.turns[k], c, s);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (ra + r < rb) {
+          s_q[(ra + r) * SM::kQPitch + k] = x1[r] * c - x2[r] * s;
+          s_q[(ra + r) * SM::kQPitch + k + D / 2] = x2[r] * c + x1[r] * s;
+        }
     }
+    for (int i = n_rows * D + tid; i < ROWS * D; i += kAqThreads) s_q[(i / D) * SM::kQPitch + i % D] = 0.f;
     __syncthreads();
     for (int r = warp; r < ROWS; r += kAqWarps) {
       float m = 0.f;
@@ -343,7 +363,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     }
     int pi[NR];  // position of the lane's score rows (-1: no such row)
 #pragma unroll
-    for (int r = 0; r < NR; ++r) pi[r] = g + 8 * r < n_rows ? i0 + (row0 + g + 8 * r) / a.G : -1;
+    for (int r = 0; r < NR; ++r) pi[r] = g + 8 * r < n_rows ? i0 + ((row0 + g + 8 * r) >> a.log_g) : -1;
 
     // ---- the stream ----
     float o[KS][NR][4];
@@ -387,8 +407,11 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
           w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
         }
 #pragma unroll
-        for (int j = 0; j < KS; ++j)
-          mma_f16(s[u], qa[j][0], qa[j][1], qa[j][2], qa[j][3], e4m3x2_to_f16x2(w[j]), e4m3x2_to_f16x2(w[j] >> 16));
+        for (int j = 0; j < KS; ++j) {
+          uint32_t b0, b1;
+          e4m3x4_to_f16x4(w[j], b0, b1);
+          mma_f16(s[u], qa[j][0], qa[j][1], qa[j][2], qa[j][3], b0, b1);
+        }
       }
       // base-2 logits with the value scale's exponent
       const float lv[2] = {__log2f(fmaxf(m.vs[0], kQ8ScaleMin)), __log2f(fmaxf(m.vs[1], kQ8ScaleMin))};
@@ -488,8 +511,9 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
           for (int e = 0; e < 4; ++e) v[e] &= keep;
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const uint32_t a0 = e4m3x2_to_f16x2(v[2 * p]), a2 = e4m3x2_to_f16x2(v[2 * p] >> 16);
-            const uint32_t a1 = e4m3x2_to_f16x2(v[2 * p + 1]), a3 = e4m3x2_to_f16x2(v[2 * p + 1] >> 16);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(v[2 * p], a0, a2);
+            e4m3x4_to_f16x4(v[2 * p + 1], a1, a3);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
               mma_f16(o[k + p][r], a0, a1, a2, a3, wh[q][r][0], wh[q][r][1]);
@@ -541,7 +565,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     }
     __syncthreads();
     const bool alone = u0 == 0 && u1 == nt;  // the whole item is here
-    const long long slot = blockIdx.x + item;
+    const uint32_t slot = blockIdx.x + item;
     for (int i = tid; i < n_rows * D; i += kAqThreads) {
       const int r = i / D, d = i % D;
       const float* p = mg + r * SM::kMPitch;
@@ -557,7 +581,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
         ls = fmaf(p[w * ROWS * SM::kMPitch + D + 1], f, ls);
       }
       if (alone) {
-        const int tok = rq.q0 + (row0 + r) / a.G, hq = h * a.G + (row0 + r) % a.G;
+        const int tok = rq.q0 + ((row0 + r) >> a.log_g), hq = h * a.G + ((row0 + r) & (a.G - 1));
         static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + d] = finish<T>(os, ls);
       } else if (slot < a.n_slots) {  // always, unless cu_q goes back and forth
         a.part[((size_t)slot * ROWS + r) * D + d] = os;
@@ -571,64 +595,73 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     __syncthreads();
     at += u1 - u0;
   }
-  if (lane == 0 && flags) atomicOr(a.pool.status, flags);
+  if (flags) atomicOr(a.pool.status, flags);
 }
 
-// Joins the partials of the items that more than one CTA worked on: one CTA an
-// item and row, one thread a dim, the partials in their order.
+// Joins the partials of the items that cuts of the line go through.  CTA column
+// x stands for the cut ahead of share x + 1 and works if that is its item's
+// first; a CTA takes one row, its warps the partials in turn.
+constexpr int kAqJoinWarps = 8;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(D) attn_q8_join_kernel(const __grid_constant__ AttnQ8Args a) {
-  griddep_wait();
-  const int R = __popcll(a.ret_mask), lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kAqJoinWarps * 32) attn_q8_join_kernel(const __grid_constant__ AttnQ8Args a) {
+  constexpr int E = D / 32;  // dims a lane
+  __shared__ float s_o[kAqJoinWarps][D], s_m[kAqJoinWarps], s_l[kAqJoinWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
+  // Everything up to the partials was there before the streaming kernel started.
   int flags = 0;
-  // item blockIdx.x: its request, KV head and row chunk (every warp for itself)
-  long long before_t = 0, before_i = 0, total = 0;
-  int b = -1;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    ReqQ8 r = {};
-    if (b0 + lane < a.B) r = load_req(a, b0 + lane, flags);
-    const long long t = r.tiles(R, a.Hkv), it = (long long)r.rc * a.Hkv;
-    const long long ts = warp_scan_ll(t), is = warp_scan_ll(it);
-    if (b < 0) {
-      const unsigned m = __ballot_sync(0xffffffffu, before_i + is > (long long)blockIdx.x);
-      if (m) {
-        const int l = __ffs(m) - 1;
-        b = b0 + l;
-        before_t = total + __shfl_sync(0xffffffffu, ts - t, l);
-        before_i += __shfl_sync(0xffffffffu, is - it, l);
-      } else {
-        before_i += __shfl_sync(0xffffffffu, is, 31);
-      }
-    }
-    total += __shfl_sync(0xffffffffu, ts, 31);
-  }
-  if (b < 0) return;
-  const ReqQ8 rq = load_req(a, b, flags);
-  const long long share = share_of(a, total);
-  const int ii = (int)(blockIdx.x - before_i), h = ii / rq.rc, rch = ii % rq.rc;
-  const int r = blockIdx.y, row = rch * a.rows + r;
-  if (row >= rq.n * a.G) return;
-  const int rb = __popcll(a.ret_mask & ((1ull << h) - 1ull));  // retrieval heads ahead of h
-  const int nt = (a.ret_mask >> h) & 1ull ? rq.tr : rq.tl;
-  const long long t0 = before_t + (long long)rq.rc * ((long long)rb * rq.tr + (long long)(h - rb) * rq.tl) + (long long)rch * nt;
-  const int c0 = (int)(t0 / share), c1 = (int)((t0 + nt - 1) / share);
-  if (c0 == c1) return;  // one CTA did it all and wrote the result
-  const float* ml = a.part_ml + (((size_t)blockIdx.x + c0) * a.rows + r) * 2;
-  const float* po = a.part + (((size_t)blockIdx.x + c0) * a.rows + r) * D + threadIdx.x;
-  const int np = c1 - c0 + 1;
-  float m = -CUDART_INF_F;
-  for (int p = lane; p < np; p += 32) m = fmaxf(m, ml[(size_t)p * a.rows * 2]);
-  m = warp_max(m);
-  const float ms = m == -CUDART_INF_F ? 0.f : m;
-  float os = 0.f, ls = 0.f;
+  const uint32_t cut = blockIdx.x + 1;
+  const LineAt line = locate(a, cut, flags);
+  griddep_wait();
+  if (line.b < 0) return;
+  const ReqQ8 rq = load_req(a, line.b, flags);
+  uint32_t rel = line.at - line.tiles;
+  const ItemAt x = item_at(a, rq, rel);
+  const int row = x.rch * a.rows + r;
+  if (rel == 0 || rel > line.share || row >= rq.n * a.G) return;  // between items, or not the first cut of its item
+  const uint32_t first = line.at - rel;  // the item's first tile on the line
+  const int np = (int)((first + (uint32_t)x.nt - 1) / line.share - (cut - 1)) + 1;  // CTAs cut - 1 and on
+  const size_t slot = (size_t)(cut - 1) + line.items + (uint32_t)(x.h * rq.rc + x.rch);
+  const float* ml = a.part_ml + (slot * a.rows + r) * 2;
+  const float* po = a.part + (slot * a.rows + r) * D + lane * E;
+  float m = -CUDART_INF_F, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
-  for (int p = 0; p < np; ++p) {
-    const float f = ex2(ml[(size_t)p * a.rows * 2] - ms);
-    os = fmaf(po[(size_t)p * a.rows * D], f, os);
-    ls = fmaf(ml[(size_t)p * a.rows * 2 + 1], f, ls);
+  for (int p = warp; p < np; p += kAqJoinWarps) {
+    const float2 y = *reinterpret_cast<const float2*>(ml + (size_t)p * a.rows * 2);
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<float2*>(v + e) = *reinterpret_cast<const float2*>(po + (size_t)p * a.rows * D + e);
+    const float mn = fmaxf(m, y.x);
+    const float f0 = m == -CUDART_INF_F ? 0.f : ex2(m - mn), f1 = mn == -CUDART_INF_F ? 1.f : ex2(y.x - mn);
+    m = mn;
+    l = l * f0 + y.y * f1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + v[e] * f1;
   }
-  const int tok = rq.q0 + row / a.G, hq = h * a.G + row % a.G;
-  static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + threadIdx.x] = finish<T>(os, ls);
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  if (tid >= D) return;
+#pragma unroll
+  for (int w = 0; w < kAqJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+  const float ms = m == -CUDART_INF_F ? 0.f : m;
+  float os = 0.f;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kAqJoinWarps; ++w) {
+    const float f = ex2(s_m[w] - ms);
+    os = fmaf(s_o[w][tid], f, os);
+    l = fmaf(s_l[w], f, l);
+  }
+  const int tok = rq.q0 + (row >> a.log_g), hq = x.h * a.G + (row & (a.G - 1));
+  static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + tid] = finish<T>(os, l);
 }
 
 // Requests of up to this many query rows a KV head (n G) are streamed, larger
@@ -663,10 +696,8 @@ long long max_items(const Shape& sh, int n_tokens, int max_q) {
   return sh.Hkv * (by_tokens < by_max ? by_tokens : by_max);
 }
 
-constexpr int kAqMaxCtas = 148 * kAqCtasPerSm;  // every SM of a B200
-
 template <typename T, int D, int ROWS>
-cudaError_t launch(const AttnQ8Args& a, long long items, cudaStream_t st) {
+cudaError_t launch(const AttnQ8Args& a, cudaStream_t st) {
   static std::mutex mu;
   static bool done[64] = {};
   int dev = 0;
@@ -681,9 +712,9 @@ cudaError_t launch(const AttnQ8Args& a, long long items, cudaStream_t st) {
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  e = launch_pdl(attn_q8_kernel<T, D, ROWS>, dim3(a.n_cta), dim3(kAqThreads), smem, st, a);
+  e = launch_pdl(attn_q8_kernel<T, D, ROWS>, dim3(kAqMaxCtas), dim3(kAqThreads), smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_q8_join_kernel<T, D>, dim3((unsigned)items, ROWS), dim3(D), 0, st, a);
+  return launch_pdl(attn_q8_join_kernel<T, D>, dim3(kAqMaxCtas - 1, ROWS), dim3(kAqJoinWarps * 32), 0, st, a);
 }
 
 }  // namespace
@@ -704,6 +735,13 @@ size_t attn_q8_workspace_bytes(const Shape& sh, int n_tokens, int max_q) {
   return bytes < 256 ? 256 : bytes;
 }
 
+// The line's positions are 32-bit numbers.
+bool attn_q8_fits(const Shape& sh, int max_q, int max_seq_len) {
+  const int q = small_q(sh, max_q);
+  const long long chunks = ((long long)q * sh.G + item_rows(sh, max_q) - 1) / item_rows(sh, max_q);
+  return (double)sh.B * sh.Hkv * (double)chunks * ((max_seq_len - 1) / kAqTile + 1) < 2147483648.0;
+}
+
 int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, const AttnQ8Call& c, void* ws,
                    cudaStream_t st) {
   AttnQ8Args a;
@@ -720,31 +758,33 @@ int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, co
   a.pool = pool;
   a.rope = rope;
   a.B = sh.B; a.Hq = sh.Hq; a.Hkv = sh.Hkv; a.G = sh.G; a.S = sh.S; a.W = sh.W;
+  a.log_g = sh.G == 1 ? 0 : sh.G == 2 ? 1 : sh.G == 4 ? 2 : 3;
   a.ret_mask = 0;
   for (int h = 0; h < sh.Hkv; ++h)
     if (sh.ret_rank[h] >= 0) a.ret_mask |= 1ull << h;
   a.c = c;
   a.rows = item_rows(sh, c.max_q);
   a.wait_ns = 400ull * 1000 * 1000;
-  for (int i = 0; i < 64; ++i) a.inv_freq[i] = sh.inv_freq[i];
+  for (int i = 0; i < 64; ++i) a.turns[i] = sh.turns[i];
   a.small_rows = small_rows(sh, c.max_q);
   const long long items = max_items(sh, c.n_tokens, c.max_q);
-  a.n_cta = kAqMaxCtas;
   a.part = static_cast<float*>(ws);
   a.n_slots = kAqMaxCtas + items;
   a.part_ml = a.part + (size_t)a.n_slots * a.rows * sh.D;
   const bool chunks = a.small_rows != INT32_MAX;
-  if (chunks)
-    chunk_carve(sh, c.n_tokens, c.max_q, a.small_rows,
-                static_cast<unsigned char*>(ws) + stream_workspace_bytes(sh, c.n_tokens, c.max_q), &a);
+  if (chunks && !chunk_carve(sh, c.n_tokens, c.max_q, a.small_rows,
+                             static_cast<unsigned char*>(ws) + stream_workspace_bytes(sh, c.n_tokens, c.max_q), &a)) {
+    set_error("attn q8: could not encode the queries' tensor map (cuTensorMapEncodeTiled)");
+    return RTP_ERR_CUDA;
+  }
   cudaError_t e = cudaSuccess;
   trace_begin(RTP_STAGE_ATTN_Q8, st);
   if (a.small_rows > 0) {
     if (sh.dtype == RTP_BF16) {
-      if (a.rows == 8) e = sh.D == 128 ? launch<__nv_bfloat16, 128, 8>(a, items, st) : launch<__nv_bfloat16, 64, 8>(a, items, st);
-      else e = sh.D == 128 ? launch<__nv_bfloat16, 128, 16>(a, items, st) : launch<__nv_bfloat16, 64, 16>(a, items, st);
+      if (a.rows == 8) e = sh.D == 128 ? launch<__nv_bfloat16, 128, 8>(a, st) : launch<__nv_bfloat16, 64, 8>(a, st);
+      else e = sh.D == 128 ? launch<__nv_bfloat16, 128, 16>(a, st) : launch<__nv_bfloat16, 64, 16>(a, st);
     } else {
-      e = sh.D == 128 ? launch<float, 128, 8>(a, items, st) : launch<float, 64, 8>(a, items, st);
+      e = sh.D == 128 ? launch<float, 128, 8>(a, st) : launch<float, 64, 8>(a, st);
     }
   }
   if (chunks && e == cudaSuccess) e = launch_attn_q8_chunks(sh, a, st);

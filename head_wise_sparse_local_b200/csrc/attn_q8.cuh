@@ -11,16 +11,21 @@ namespace rtp {
 constexpr float kAqRescale = 8.f;  // the running maximum moves when a tile exceeds it by 2^8
 constexpr float kAqLift = 6.f;     // weights are held 2^6 up (at most 2^14 in fp16), away from fp16's small end
 
-// 256 query rows of one (request, KV head).
-struct ChunkItem {
-  int b, h, grp, tiles;
+// 256 query rows of one (request, KV head): row r is token (row0 + r) / G of
+// the request, at position i0 + that, and query head (row0 + r) % G of the
+// group.  Its tiles of 128 positions are [0, ns) and from w0 on.
+struct __align__(16) ChunkItem {
+  int b, h, row0, n_rows;
+  int q0, i0, i_hi, tiles;  // first packed row, its position; position of the item's last row
+  int ns, w0, ret, pad;
 };
 
 struct __align__(64) AttnQ8Args {
   CUtensorMap tm_k, tm_v;  // the pool as [n_blocks Hkv block_size][D] bytes, boxes of min(32, block_size) rows
   Q8Pool pool;
   RopeAxes rope;
-  int B, Hq, Hkv, G, S, W, rows, n_cta;
+  int B, Hq, Hkv, G, S, W, rows;
+  int log_g;          // G is a power of two
   int small_rows;     // requests of more query rows (n G) a KV head go to the chunk kernel
   long long n_slots;  // partials that the workspace holds
   uint64_t ret_mask;
@@ -28,14 +33,18 @@ struct __align__(64) AttnQ8Args {
   float* part;  // [n_cta + items][rows][D] O, then [..][rows][2] (M, l)
   float* part_ml;
   unsigned long long wait_ns;
-  double inv_freq[64];
+  uint64_t turns[64];  // rotary frequencies
   // the chunk kernel's share of the workspace
-  struct ChunkItem* items;
-  long long* prefix;  // tiles ahead of each item, then their number
+  ChunkItem* items;
+  long long* prefix;  // tiles ahead of each item, then their number; [max_chunk_items + 1]: a CTA's share of them
   int* req_items;     // [B + 1] items ahead of each request
   float* cpart;       // partials of cut items: [2 CTAs][256][D], and (M, l)
   float* cpart_ml;
   int max_chunk_items;
+  __half* cq;         // rotated queries, [n_tokens][Hq][D], each row by its power-of-two scale
+  float* cq_unit;     // [n_tokens][Hq]: from their products to base-2 logits
+  CUtensorMap tm_q;   // cq, boxes of 64 dims x G heads x 128 / G tokens
+  CUtensorMap tm_ck, tm_cv;  // the pool as rows of D bytes, boxes of min(64, block_size) rows
 };
 
 
@@ -88,7 +97,7 @@ __device__ __forceinline__ T finish(float o, float l) {
 // The chunk kernel (bf16 layers): workspace, and its launches for the requests
 // of more than a.small_rows query rows a KV head.
 size_t chunk_workspace_bytes(const Shape& sh, int n_tokens, int max_q, int small_rows);
-void chunk_carve(const Shape& sh, int n_tokens, int max_q, int small_rows, void* ws, AttnQ8Args* a);
+bool chunk_carve(const Shape& sh, int n_tokens, int max_q, int small_rows, void* ws, AttnQ8Args* a);
 cudaError_t launch_attn_q8_chunks(const Shape& sh, const AttnQ8Args& a, cudaStream_t st);
 
 }  // namespace rtp

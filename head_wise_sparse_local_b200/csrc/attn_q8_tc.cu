@@ -15,19 +15,26 @@
 // load the SMs evenly.  A cut item leaves partials that a second kernel joins.  A first,
 // one-CTA kernel lays the line out.
 //
-// Roles (13 warps):
+// Roles (16 warps):
 //   warps 0-3, 4-7   the softmax of slot 0 and slot 1 (128 rows each), one
-//                    thread a row: its weights against the running maximum as
-//                    S is read from TMEM once, kept packed in registers until
-//                    the tile's maximum is known not to exceed it by 2^8 (else
-//                    O is rescaled and the weights formed again), then written
-//                    over S in TMEM;
-//   warps 8-11       fetch K and V from their blocks into registers one tile
-//                    ahead, convert e4m3 to fp16 and store the operands' swizzled layout
-//                    (fetching through registers and not by TMA saves a pass
-//                    through shared memory, whose bandwidth the products need);
+//                    thread a row: weights against the running maximum as S is
+//                    read from TMEM, written over the columns already read;
+//                    where 32 columns exceed the maximum by 2^9, it moves, and O
+//                    and the tile's weights so far are rescaled (holding
+//                    the row in registers to find its maximum first took
+//                    straight-line code that the instruction cache could not
+//                    feed: 8100 clocks a tile; reading S twice, 5650);
+//   warps 8-11       convert a tile's e4m3 rows to fp16 in the operands' swizzled layout;
 //   warp 12          issues the products in the order S0(i), PV1(i-1), S1(i),
-//                    PV0(i): each slot's softmax runs beside the other's products.
+//                    PV0(i): each slot's softmax runs beside the other's products;
+//   warp 13          loads by TMA: Q of the next item, K and V rows of the next
+//                    tile from their blocks, and reads the blocks' scales.
+// The roles run on from item to item on their own; nothing synchronises the CTA
+// between its first and its last tile.
+//
+// The first kernel also rotates the queries: fp16 rows and their scales, once
+// a token, not once a CTA in a prologue that stalls its products (33000 clocks an
+// item, measured).
 //
 // Every wait is bounded: on expiry the CTA sets RTP_DEV_TIMEOUT, stops issuing,
 // waits (bounded) for what it issued and frees its TMEM.
@@ -39,6 +46,7 @@
 
 #include "attn_q8.cuh"
 #include "tc.cuh"
+#include "tensor_map.h"
 
 namespace rtp {
 namespace {
@@ -46,11 +54,12 @@ namespace {
 constexpr int kCRows = 128;               // query rows a slot = TMEM lanes
 constexpr int kCGroup = 256;              // query rows an item
 constexpr int kCKeys = 128;               // positions a tile
-constexpr int kCThreads = 13 * 32;
+constexpr int kCThreads = 16 * 32;
 constexpr int kCRegion = 128 * 128;       // bytes of 128 rows x 64 fp16 dims
 constexpr int kCCtas = 148;               // one an SM of a B200
 constexpr int kCMinShare = 4;             // tiles a CTA takes at least: a segment's start and end cost about as much
 constexpr int kCTmemCols = 512;
+constexpr float kCRescale = 9.f;          // the running maximum moves past 2^9: weights reach 2^15, below fp16's largest
 
 template <int D>
 struct CSmem {
@@ -58,7 +67,9 @@ struct CSmem {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = 2 * kOp;
   static constexpr int kOffV = kOffK + 2 * kOp;
-  static constexpr int kBytes = kOffV + 2 * kOp + 1024;  // + alignment slack
+  static constexpr int kRaw = kCKeys * D;          // e4m3 rows of a tile
+  static constexpr int kOffRaw = kOffV + 2 * kOp;  // K, then V
+  static constexpr int kBytes = kOffRaw + 2 * kRaw + 1024;  // + alignment slack
 };
 
 // Scales of 16 positions of a tile, and which 32-position words are there.
@@ -67,41 +78,32 @@ struct __align__(16) CMeta {
   uint32_t there[4];
 };
 
-// An item's geometry.
-struct CItem {
-  int q0, n, i0, n_rows, row0, i_lo, i_hi, ns, w0, tiles;
-  bool ret;
-  __device__ __forceinline__ int key(int u) const { return (ret || u < ns ? u : w0 + u - ns) * kCKeys; }
-};
+// First position of an item's u-th tile.
+__device__ __forceinline__ int tile_pos(const ChunkItem& c, int u) { return (u < c.ns ? u : c.w0 + u - c.ns) * kCKeys; }
 
-__device__ __forceinline__ CItem chunk_item(const AttnQ8Args& a, const ReqRows& r, int h, int grp) {
-  CItem c;
-  c.q0 = r.q0;
-  c.n = r.n;
-  c.i0 = r.L - r.n;
+__device__ __forceinline__ ChunkItem chunk_item(const AttnQ8Args& a, const ReqRows& r, int b, int h, int grp) {
+  ChunkItem c;
+  c.b = b;
+  c.h = h;
   c.row0 = grp * kCGroup;
   c.n_rows = min(kCGroup, r.n * a.G - c.row0);
-  c.i_lo = c.i0 + c.row0 / a.G;
-  c.i_hi = c.i0 + (c.row0 + c.n_rows - 1) / a.G;
-  c.ret = (a.ret_mask >> h) & 1ull;
+  c.q0 = r.q0;
+  c.i0 = r.L - r.n;
+  c.i_hi = c.i0 + ((c.row0 + c.n_rows - 1) >> a.log_g);
+  c.ret = (int)((a.ret_mask >> h) & 1ull);
+  c.pad = 0;
   const int nt = c.i_hi / kCKeys + 1;
   c.ns = min((a.S + kCKeys - 1) / kCKeys, nt);
-  c.w0 = max(0, c.i_lo - a.W + 1) / kCKeys;
-  if (c.ret || c.w0 <= c.ns) {
-    c.ns = c.w0 = 0;
-    c.tiles = nt;
-  } else {
-    c.tiles = c.ns + nt - c.w0;
-  }
+  c.w0 = max(0, c.i0 + (c.row0 >> a.log_g) - a.W + 1) / kCKeys;
+  if (c.ret || c.w0 <= c.ns) c.ns = c.w0 = 0;
+  c.tiles = c.ns + nt - c.w0;
   return c;
 }
 
-__device__ __forceinline__ long long chunk_share(long long total) {
-  return max((total + kCCtas - 1) / kCCtas, (long long)kCMinShare);
-}
+constexpr int kCPrep = 256;  // threads of the first kernel
 
-// Exclusive scan over the block (1024 threads) and its total.
-__device__ __forceinline__ long long block_scan_1024(long long v, long long& total, long long* s_warp) {
+// Exclusive scan over the block and its total.
+__device__ __forceinline__ long long block_scan(long long v, long long& total, long long* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
 #pragma unroll
@@ -112,23 +114,79 @@ __device__ __forceinline__ long long block_scan_1024(long long v, long long& tot
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  long long w = s_warp[lane], ws = w;
+  long long before = 0;
+  total = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, ws, o);
-    if (lane >= o) ws += y;
+  for (int w = 0; w < kCPrep / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
   }
-  total = __shfl_sync(0xffffffffu, ws, 31);
-  return x - v + __shfl_sync(0xffffffffu, ws - w, warp);
+  return x - v + before;
 }
 
-// The line: items in the order (request, KV head, group), and the tiles ahead of each.
-__global__ void __launch_bounds__(1024) chunk_line_kernel(const __grid_constant__ AttnQ8Args a) {
-  __shared__ long long s_warp[32];
+// Block 0 lays out the line: items in the order (request, KV head, group), and
+// the tiles ahead of each.  The others rotate queries: a warp a token and 8
+// heads; every row becomes fp16 of its power-of-two scale, and its factor from
+// products to base-2 logits.
+template <int D>
+__global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constant__ AttnQ8Args a) {
+  if (blockIdx.x > 0) {
+    constexpr int PP = D / 64, H = D / 2;
+    const int lane = threadIdx.x & 31;
+    const int hb = (a.Hq + 7) / 8;
+    const long long task = (long long)(blockIdx.x - 1) * (kCPrep / 32) + (threadIdx.x >> 5);
+    griddep_wait();
+    griddep_launch();
+    if (task >= (long long)a.c.n_tokens * hb) return;
+    const int t = (int)(task / hb), h0 = (int)(task % hb) * 8;
+    const float unit = 1.4426950408889634f * rsqrtf((float)D);
+    float c[PP], s[PP];
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      const int k = lane * PP + i;
+      rope_turns(a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + t], a.turns[k], c[i], s[i]);
+    }
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.c.q_pre) + (size_t)t * a.c.q_stride + (size_t)h0 * D + lane * PP;
+    const int nh = min(a.Hq - h0, 8);
+    float x1[8][PP], x2[8][PP];
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < nh) {
+#pragma unroll
+        for (int i = 0; i < PP; ++i) {
+          x1[h][i] = to_f32(q[h * D + i]);
+          x2[h][i] = to_f32(q[h * D + H + i]);
+        }
+      }
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      if (h >= nh) break;
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < PP; ++i) {
+        const float y1 = x1[h][i] * c[i] - x2[h][i] * s[i];
+        x2[h][i] = x2[h][i] * c[i] + x1[h][i] * s[i];
+        x1[h][i] = y1;
+        m = fmaxf(m, fmaxf(fabsf(y1), fabsf(x2[h][i])));
+      }
+      const float sc = query_scale(warp_max(m)), inv = 1.f / sc;
+      const size_t row = (size_t)t * a.Hq + h0 + h;
+      __half* o = a.cq + row * D + lane * PP;
+#pragma unroll
+      for (int i = 0; i < PP; ++i) {
+        o[i] = __float2half_rn(x1[h][i] * inv);
+        o[H + i] = __float2half_rn(x2[h][i] * inv);
+      }
+      if (lane == 0) a.cq_unit[row] = sc * unit;
+    }
+    return;
+  }
+  __shared__ long long s_warp[kCPrep / 32];
   griddep_wait();
+  griddep_launch();
   int flags = 0;
   long long n_items = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 1024) {
+  for (int b0 = 0; b0 < a.B; b0 += kCPrep) {
     const int b = b0 + threadIdx.x;
     long long v = 0;
     if (b < a.B) {
@@ -137,7 +195,7 @@ __global__ void __launch_bounds__(1024) chunk_line_kernel(const __grid_constant_
       if (rows > a.small_rows) v = a.Hkv * ((rows + kCGroup - 1) / kCGroup);
     }
     long long total;
-    const long long x = n_items + block_scan_1024(v, total, s_warp);
+    const long long x = n_items + block_scan(v, total, s_warp);
     if (b < a.B) a.req_items[b] = (int)min(x, (long long)a.max_chunk_items);
     n_items += total;
   }
@@ -145,10 +203,10 @@ __global__ void __launch_bounds__(1024) chunk_line_kernel(const __grid_constant_
   if (threadIdx.x == 0) a.req_items[a.B] = (int)n_items;
   __syncthreads();
   long long tiles = 0;
-  for (int i0 = 0; i0 < n_items; i0 += 1024) {
+  for (int i0 = 0; i0 < n_items; i0 += kCPrep) {
     const int i = i0 + threadIdx.x;
     long long v = 0;
-    ChunkItem it = {0, 0, 0, 0};
+    ChunkItem it = {};
     if (i < n_items) {
       int b = 0, hi = a.B;  // the last request with req_items <= i
       while (hi - b > 1) {
@@ -158,21 +216,21 @@ __global__ void __launch_bounds__(1024) chunk_line_kernel(const __grid_constant_
       }
       const ReqRows r = load_rows(a, b, flags);
       const int ng = (r.n * a.G + kCGroup - 1) / kCGroup, rel = i - a.req_items[b];
-      it.b = b;
-      it.h = rel / ng;
-      it.grp = rel % ng;
-      it.tiles = chunk_item(a, r, it.h, it.grp).tiles;
+      it = chunk_item(a, r, b, rel / ng, rel % ng);
       v = it.tiles;
     }
     long long total;
-    const long long x = tiles + block_scan_1024(v, total, s_warp);
+    const long long x = tiles + block_scan(v, total, s_warp);
     if (i < n_items) {
       a.items[i] = it;
       a.prefix[i] = x;
     }
     tiles += total;
   }
-  if (threadIdx.x == 0) a.prefix[n_items] = tiles;
+  if (threadIdx.x == 0) {
+    a.prefix[n_items] = tiles;
+    a.prefix[a.max_chunk_items + 1] = max((tiles + kCCtas - 1) / kCCtas, (long long)kCMinShare);
+  }
   if (flags) atomicOr(a.pool.status, flags);
 }
 
@@ -208,47 +266,160 @@ __device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {  //
       : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
 
-__device__ __forceinline__ bool c_wait(uint64_t* bar, uint32_t parity, const AttnQ8Args& a, volatile int* s_abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+// (x, y) = (2^x, 2^y) on the FMA pipe, the cubic of ex2_poly on a pair.
+__device__ __forceinline__ void ex2_poly2(float& x, float& y) {
+  const float a = fmaxf(x, -125.f), b = fmaxf(y, -125.f);
+  asm("{\n\t.reg .b64 v, t, f, p, c;\n\t.reg .b32 t0, t1, p0, p1;\n\t"
+      "mov.b64 v, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\tadd.rn.f32x2 t, v, c;\n\t"    // round(x) in t's low bits
+      "mov.b64 c, {%5, %5};\n\tadd.rn.f32x2 f, t, c;\n\t"
+      "mov.b64 c, {%6, %6};\n\tfma.rn.f32x2 f, f, c, v;\n\t"                          // x - round(x)
+      "mov.b64 c, {%7, %7};\n\tmov.b64 p, {%8, %8};\n\tfma.rn.f32x2 p, p, f, c;\n\t"
+      "mov.b64 c, {%9, %9};\n\tfma.rn.f32x2 p, p, f, c;\n\t"
+      "mov.b64 c, {%10, %10};\n\tfma.rn.f32x2 p, p, f, c;\n\t"
+      "mov.b64 {t0, t1}, t;\n\tmov.b64 {p0, p1}, p;\n\t"
+      "shl.b32 t0, t0, 23;\n\tshl.b32 t1, t1, 23;\n\tadd.s32 p0, p0, t0;\n\tadd.s32 p1, p1, t1;\n\t"
+      "mov.b32 %0, p0;\n\tmov.b32 %1, p1;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(12582912.f), "f"(-12582912.f), "f"(-1.f), "f"(0.24261111f), "f"(0.05517161f),
+        "f"(0.69326097f), "f"(0.99992806f));
+}
+
+__device__ __noinline__ bool c_wait_long(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, int* status,
+                                         volatile int* s_abort) {
   const unsigned long long t0 = global_ns();
   while (!mbar_try_wait_sleep(bar, parity, kWaitHintNs)) {
     if (*s_abort) return false;
-    if (global_ns() - t0 > a.wait_ns) {
+    if (global_ns() - t0 > limit_ns) {
       *s_abort = 1;
-      atomicOr(a.pool.status, RTP_DEV_TIMEOUT);
+      atomicOr(status, RTP_DEV_TIMEOUT);
       return false;
     }
   }
+  return true;
+}
+// Bounded wait that also gives up once another role has; the warp agrees on the outcome.
+__device__ __forceinline__ bool c_wait(uint64_t* bar, uint32_t parity, const AttnQ8Args& a, volatile int* s_abort) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = c_wait_long(bar, parity, a.wait_ns, a.pool.status, s_abort);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* tm, int y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+               :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(0), "r"(y)
+               : "memory");
+}
+
+// The CTA's share of the line, walked item by item (each role for itself).
+struct CWalk {
+  int item;
+  long long at, end;
+  // the current segment: tiles [u0, u0 + nt) of item c
+  ChunkItem c;
+  int u0, nt;
+  bool two;  // it has rows for the second slot
+  __device__ __forceinline__ bool start(const AttnQ8Args& a) {
+    const int n_items = a.req_items[a.B];
+    const long long total = a.prefix[n_items], share = a.prefix[a.max_chunk_items + 1];
+    at = (long long)blockIdx.x * share;
+    end = min(total, at + share);
+    if (at >= end) return false;
+    item = find_item(a.prefix, n_items, at);
+    load(a);
+    return true;
+  }
+  __device__ __forceinline__ void load(const AttnQ8Args& a) {
+    c = a.items[item];
+    u0 = (int)(at - a.prefix[item]);
+    nt = (int)min((long long)c.tiles - u0, end - at);
+    two = c.n_rows > kCRows;
+  }
+  __device__ __forceinline__ bool next(const AttnQ8Args& a) {
+    at += nt;
+    ++item;
+    if (at >= end) return false;
+    load(a);
+    return true;
+  }
+};
+
+struct CBars {
+  uint64_t raw_full[2], raw_empty[2];                       // K's rows as stored, and V's
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];    // by stage
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];  // by slot
+  uint64_t fin;
+};
+
+// Asks for the rows of the CTA's tile T, whose blocks the lanes hold in `id`, and writes its scales.
+template <int D>
+__device__ __forceinline__ bool load_rows_of_tile(const AttnQ8Args& a, const CWalk& w, int T, int id, CBars& bars,
+                                                  unsigned char* raw, CMeta* meta, volatile int* s_abort, uint32_t (&asked)[2]) {
+  const int lane = threadIdx.x & 31;
+  const int per = kCKeys >> a.pool.log_bs, box = 1 << a.pool.log_bs;  // copies a tile, of so many rows
+  float ks = 0.f, vs = 0.f;
+  if (id >= 0) {
+    ks = a.pool.k_scale[(size_t)id * a.Hkv + w.c.h];
+    vs = a.pool.v_scale[(size_t)id * a.Hkv + w.c.h];
+  }
+  // copy p < per covers the blocks of lanes p * 8 / per ..; a block that is not there: any rows, they become zeros
+  const int mine = __shfl_sync(0xffffffffu, id, (lane & 7) * (8 / per) & 7);
+  const int y = (((mine < 0 ? 0 : mine) * a.Hkv + w.c.h) << a.pool.log_bs);  // (a tile starts on a block)
+  if (!c_wait(&bars.raw_empty[0], ((uint32_t)T & 1u) ^ 1u, a, s_abort)) return false;
+  CMeta& m = meta[T & 7];
+  const unsigned there = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
+  vs = fmaxf(vs, kQ8ScaleMin);
+  if (lane < 8) m.g[lane] = make_float4(fmaxf(ks, kQ8ScaleMin), __log2f(vs), 1.f / vs, 0.f);
+  if (lane < 4)
+    m.there[lane] = ((there >> (2 * lane) & 1u) ? 0xffffu : 0u) | ((there >> (2 * lane + 1) & 1u) ? 0xffff0000u : 0u);
+  __syncwarp();
+  if (lane == 0) mbar_expect_tx(&bars.raw_full[0], (uint32_t)(kCKeys * D));
+  __syncwarp();
+  if (lane < per) tma_rows(raw + lane * box * D, &a.tm_ck, y, &bars.raw_full[0]);
+  ++asked[0];
+  if (!c_wait(&bars.raw_empty[1], ((uint32_t)T & 1u) ^ 1u, a, s_abort)) return false;
+  if (lane == 0) mbar_expect_tx(&bars.raw_full[1], (uint32_t)(kCKeys * D));
+  __syncwarp();
+  if (lane < per) tma_rows(raw + kCKeys * D + lane * box * D, &a.tm_cv, y, &bars.raw_full[1]);
+  ++asked[1];
   return true;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __grid_constant__ AttnQ8Args a) {
   using SM = CSmem<D>;
-  constexpr int H = D / 2;
   extern __shared__ __align__(1024) unsigned char dsm_raw[];
-  __shared__ __align__(8) uint64_t bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2];
-  __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_full[2], bar_o_done, bar_fin;
-  // tile i's scales, read by the softmax after S(i); rewritten for tile i + 4, after S1(i + 2)
-  // has completed, which follows both slots' weights of tile i + 1
-  __shared__ CMeta s_meta[4];
+  __shared__ __align__(8) CBars bars;
+  // tile i's scales, read by the softmax after S(i); rewritten for tile i + 8, whose rows are
+  // asked for once tile i + 7 is converted, S of tile i + 5 complete and the weights of tile i + 4 formed
+  __shared__ CMeta s_meta[8];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_item;
+  __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned char* dsm = dsm_raw + ((1024u - (smem_u32(dsm_raw) & 1023u)) & 1023u);
-  const uint32_t sQ = smem_u32(dsm + SM::kOffQ), sK = smem_u32(dsm + SM::kOffK), sV = smem_u32(dsm + SM::kOffV);
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar_k_full[s], 128);
-      mbar_init(&bar_k_empty[s], 1);
-      mbar_init(&bar_v_full[s], 128);
-      mbar_init(&bar_v_empty[s], 1);
-      mbar_init(&bar_s_full[s], 2);  // the products' commit, and the issuer (who has seen the scales)
-      mbar_init(&bar_p_full[s], kCRows);
+      mbar_init(&bars.raw_full[s], 1);
+      mbar_init(&bars.raw_empty[s], 128);
+      mbar_init(&bars.k_full[s], 128);
+      mbar_init(&bars.k_empty[s], 1);
+      mbar_init(&bars.v_full[s], 128);
+      mbar_init(&bars.v_empty[s], 1);
+      mbar_init(&bars.q_full[s], 1);
+      mbar_init(&bars.q_empty[s], 1);
+      mbar_init(&bars.s_full[s], 2);  // the products' commit, and the issuer (who has seen the scales)
+      mbar_init(&bars.p_full[s], kCRows);
+      mbar_init(&bars.o_full[s], 1);
+      mbar_init(&bars.o_empty[s], kCRows);
     }
-    mbar_init(&bar_o_done, 1);
-    mbar_init(&bar_fin, 1);
+    mbar_init(&bars.fin, 1);
     s_abort = 0;
   }
   if (warp == 12) {
@@ -261,266 +432,39 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   griddep_wait();
+  griddep_launch();
 
-  const int n_items = a.req_items[a.B];
-  const long long total = a.prefix[n_items], share = chunk_share(total);
-  long long at = (long long)blockIdx.x * share;
-  const long long end = min(total, at + share);
-  int flags = 0;
-  // tiles so far: phases of the K and V stages, and of each slot's barriers (slot 1 idles where an item has no row for it)
-  int gt = 0, gs1 = 0;
-  uint32_t seg_par = 0u;
-  if (at < end && warp == 0) {
-    const int it = find_item(a.prefix, n_items, at);
-    if (lane == 0) s_item = it;
-  }
-  __syncthreads();
-  int item = s_item;
-
-  while (at < end) {
-    const ChunkItem ci = a.items[item];
-    int dummy = 0;
-    const ReqRows rr = load_rows(a, ci.b, dummy);
-    const CItem c = chunk_item(a, rr, ci.h, ci.grp);
-    const int h = ci.h;
-    const int u0 = (int)(at - a.prefix[item]);
-    const int nt = (int)min((long long)c.tiles - u0, end - at);  // tiles [u0, u0 + nt) of the item
-    const bool two = c.n_rows > kCRows;
-    // ---- Q: cos and sin of the item's tokens (over the K stages), then each
-    // row rotated, scaled by its power of two and stored as fp16, swizzled ----
-    float2* s_cs = reinterpret_cast<float2*>(dsm + SM::kOffK);
-    const int tok0 = c.row0 / a.G, n_tok = (c.row0 + c.n_rows - 1) / a.G - tok0 + 1;
-    float rs = 1.f;  // the thread's row: factor from products to base-2 logits
-    static_assert(4 * SM::kOp >= kCGroup * H * (int)sizeof(float2), "the table fits over the K and V stages");
-    for (int i = tid; i < n_tok * H; i += kCThreads) {
-      const int t = c.q0 + tok0 + i / H, k = i % H;
-      float2 cs;
-      rope_cos_sin(a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + t], a.inv_freq[k], cs.x, cs.y);
-      s_cs[i] = cs;
-    }
-    __syncthreads();
-    if (warp < 8) {
-      const int r = tid;  // row of the item
-      unsigned char* qs = dsm + SM::kOffQ + (r / kCRows) * SM::kOp + (r % kCRows) * 128;
-      if (r < c.n_rows) {
-        const int tl = (c.row0 + r) / a.G - tok0;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.c.q_pre) +
-                                 (size_t)(c.q0 + tok0 + tl) * a.c.q_stride + (size_t)(h * a.G + (c.row0 + r) % a.G) * D;
-        const float2* cs = s_cs + tl * H;
-        float m = 0.f;
-#pragma unroll 2
-        for (int k8 = 0; k8 < H; k8 += 8) {
-          float x1[8], x2[8];
-          load_row<__nv_bfloat16, 8>(q + k8, x1);
-          load_row<__nv_bfloat16, 8>(q + H + k8, x2);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 f = cs[k8 + e];
-            m = fmaxf(m, fmaxf(fabsf(x1[e] * f.x - x2[e] * f.y), fabsf(x2[e] * f.x + x1[e] * f.y)));
-          }
-        }
-        const float s = query_scale(m), inv = 1.f / s;
-        rs = s * (1.4426950408889634f * rsqrtf((float)D));
-#pragma unroll 2
-        for (int k8 = 0; k8 < H; k8 += 8) {
-          float x1[8], x2[8];
-          load_row<__nv_bfloat16, 8>(q + k8, x1);
-          load_row<__nv_bfloat16, 8>(q + H + k8, x2);
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 f = cs[k8 + e], g = cs[k8 + e + 1];
-            lo[e / 2] = pack_f16((x1[e] * f.x - x2[e] * f.y) * inv, (x1[e + 1] * g.x - x2[e + 1] * g.y) * inv);
-            hi[e / 2] = pack_f16((x2[e] * f.x + x1[e] * f.y) * inv, (x2[e + 1] * g.x + x1[e + 1] * g.y) * inv);
-          }
-          const int d1 = k8, d2 = H + k8;
-          *reinterpret_cast<uint4*>(qs + (d1 / 64) * kCRegion + ((((d1 % 64) / 8) ^ (r & 7)) * 16)) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *reinterpret_cast<uint4*>(qs + (d2 / 64) * kCRegion + ((((d2 % 64) / 8) ^ (r & 7)) * 16)) =
-              make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        }
-      } else if (r < kCRows || two) {  // rows that the item does not have
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          *reinterpret_cast<uint4*>(qs + (k / 8) * kCRegion + (k % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    fence_async_smem();
-    __syncthreads();
-
-    if (warp >= 8 && warp < 12) {
-      // ---- K and V: fetched a tile ahead, converted, stored ----
-      constexpr int LPR = D / 16;          // lanes a row (16 bytes each)
-      constexpr int RPI = 4 * (32 / LPR);  // rows the four warps fetch at once
-      constexpr int IT = kCKeys / RPI;
-      const int cw = warp - 8;
-      const int r_lane = cw * (32 / LPR) + lane / LPR, cl = lane % LPR;
-      const int bs1 = (1 << a.pool.log_bs) - 1;
-      const int* tab = a.c.block_table + (size_t)ci.b * a.pool.table_cols;
-      // lane g < 8: the block of positions [16 g, 16 g + 16) of tile u, -1 if it has none
-      auto block_id = [&](int u) {
-        const int j = c.key(u) + 16 * (lane & 7);
-        if (j > c.i_hi) return -1;
-        const int id = tab[j >> a.pool.log_bs];
-        if ((unsigned)id < (unsigned)a.pool.n_blocks) return id;
-        flags |= RTP_DEV_BLOCKS;
-        return -1;
-      };
-      auto fetch = [&](const void* pool, int u, int id, uint4 (&x)[IT]) {
-        const int j0 = c.key(u);
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int r = i * RPI + r_lane, j = j0 + r;
-          const int blk = __shfl_sync(0xffffffffu, id, r >> 4);
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (blk >= 0 && j <= c.i_hi)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(pool) +
-                         (((((size_t)blk * a.Hkv + h) << a.pool.log_bs) + (j & bs1)) * D + cl * 16)));
-        }
-      };
-      auto store = [&](unsigned char* dst, const uint4 (&x)[IT]) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int r = i * RPI + r_lane;
-          const uint4 lo = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16),
-                                      e4m3x2_to_f16x2(x[i].y), e4m3x2_to_f16x2(x[i].y >> 16));
-          const uint4 hi = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
-                                      e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
-          // 16 dims are two 16-byte chunks of a 64-dim region; lanes of the two
-          // regions take them in opposite order, so eight lanes hit eight chunks
-          const int reg = cl >> 2, ch = (2 * cl) & 7, odd = reg & 1;
-          unsigned char* p = dst + reg * kCRegion + r * 128;
-          *reinterpret_cast<uint4*>(p + (((ch + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(p + (((ch + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
-        }
-      };
-      uint4 xk[IT], xv[IT];
-      int id = block_id(u0);
-      fetch(a.pool.k, u0, id, xk);
-      fetch(a.pool.v, u0, id, xv);
-      float ks = 0.f, vs = 0.f;
-      if (cw == 0 && id >= 0) {
-        ks = a.pool.k_scale[(size_t)id * a.Hkv + h];
-        vs = a.pool.v_scale[(size_t)id * a.Hkv + h];
-      }
-      for (int i = 0; i < nt; ++i) {
-        const int T = gt + i, st = T & 1;
-        const uint32_t par = ((uint32_t)(T >> 1) & 1u) ^ 1u;
-        const int id_next = i + 1 < nt ? block_id(u0 + i + 1) : -1;
-        if (!__all_sync(0xffffffffu, c_wait(&bar_k_empty[st], par, a, &s_abort))) break;
-        store(dsm + SM::kOffK + st * SM::kOp, xk);
-        if (cw == 0) {
-          CMeta& m = s_meta[T & 3];
-          const unsigned there = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
-          vs = fmaxf(vs, kQ8ScaleMin);
-          if (lane < 8) m.g[lane] = make_float4(fmaxf(ks, kQ8ScaleMin), __log2f(vs), 1.f / vs, 0.f);
-          if (lane < 4) m.there[lane] = ((there >> (2 * lane) & 1u) ? 0xffffu : 0u) | ((there >> (2 * lane + 1) & 1u) ? 0xffff0000u : 0u);
-          ks = vs = 0.f;
-          if (id_next >= 0) {
-            ks = a.pool.k_scale[(size_t)id_next * a.Hkv + h];
-            vs = a.pool.v_scale[(size_t)id_next * a.Hkv + h];
-          }
-        }
-        if (i + 1 < nt) fetch(a.pool.k, u0 + i + 1, id_next, xk);
-        fence_async_smem();
-        mbar_arrive(&bar_k_full[st]);
-        if (!__all_sync(0xffffffffu, c_wait(&bar_v_empty[st], par, a, &s_abort))) break;
-        store(dsm + SM::kOffV + st * SM::kOp, xv);
-        if (i + 1 < nt) fetch(a.pool.v, u0 + i + 1, id_next, xv);
-        fence_async_smem();
-        mbar_arrive(&bar_v_full[st]);
-        id = id_next;
-      }
-    } else if (warp == 12) {
-      // ---- the products ----
-      constexpr uint32_t idS = umma_idesc(kCRows, kCKeys, false, true);
-      constexpr uint32_t idO = umma_idesc(kCRows, D, true, true);
-      const uint32_t tS[2] = {tmem, tmem + kCKeys};
-      const uint32_t tO[2] = {tmem + 2 * kCKeys, tmem + 3 * kCKeys};
-      const uint64_t dq0 = umma_desc(sQ, 16, 1024), dk0 = umma_desc(sK, 16, 1024), dv0 = umma_desc(sV, kCRegion, 1024);
-      auto issue_s = [&](int slot, int st) {
-        if (lane == 0) {
-          const uint64_t dq = dq0 + (uint64_t)((slot * SM::kOp) >> 4), dk = dk0 + (uint64_t)((st * SM::kOp) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (uint32_t)(((kk / 4) * kCRegion + (kk % 4) * 32) >> 4);
-            umma_f16(tS[slot], dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
-          }
-          mbar_arrive(&bar_s_full[slot]);
-          umma_commit(&bar_s_full[slot]);
-        }
-        __syncwarp();
-      };
-      auto issue_pv = [&](int slot, int st, bool acc) {
-        if (lane == 0) {
-          const uint64_t dv = dv0 + (uint64_t)((st * SM::kOp) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kCKeys / 16; ++kk)
-            umma_f16_ts(tO[slot], tS[slot] + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idO, (acc || kk > 0) ? 1u : 0u);
-        }
-        __syncwarp();
-      };
-      auto wait = [&](uint64_t* bar, uint32_t par) {
-        const bool ok = __all_sync(0xffffffffu, c_wait(bar, par, a, &s_abort));
+  if (warp < 8) {
+    // ---- softmax: one thread a row ----
+    const int slot = warp >> 2, quad = warp & 3, r = tid;  // row of the item
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tSs = tmem + slot * kCKeys + lane_off, tOs = tmem + (2 + slot) * kCKeys + lane_off;
+    uint32_t ph = 0u, seg = 0u;  // tiles and items of this slot so far
+    int gt = 0;                  // tiles of the CTA
+    CWalk w;
+    bool ok = true;
+    for (bool more = w.start(a); more && ok; gt += w.nt, more = w.next(a)) {
+      if (slot == 1 && !w.two) continue;
+      const ChunkItem& c = w.c;
+      const bool rv = r < c.n_rows;
+      const int pi = c.i0 + ((c.row0 + r) >> a.log_g);                // the row's position
+      const int s_lo = c.i0 + ((c.row0 + slot * kCRows) >> a.log_g);  // the slot's first, and its last row's
+      const int s_hi = min(c.i_hi, c.i0 + ((c.row0 + slot * kCRows + kCRows - 1) >> a.log_g));
+      const int tok = c.q0 + ((c.row0 + r) >> a.log_g), hq = w.c.h * a.G + ((c.row0 + r) & (a.G - 1));
+      const float rs = rv ? a.cq_unit[(size_t)tok * a.Hq + hq] : 1.f;
+      float M = -CUDART_INF_F, l = 0.f;
+      bool poison = false;
+      for (int i = 0; i < w.nt; ++i, ph ^= 1u) {
+        const int kt = tile_pos(c, w.u0 + i);
+        if (!c_wait(&bars.s_full[slot], ph, a, &s_abort)) { ok = false; break; }
         tc_fence_after();
-        return ok;
-      };
-      bool ok = true;
-      for (int i = 0; i < nt && ok; ++i) {
-        const int T = gt + i, st = T & 1;
-        const uint32_t par = (uint32_t)(T >> 1) & 1u;
-        ok = wait(&bar_k_full[st], par);
-        if (!ok) break;
-        issue_s(0, st);
-        if (two) {
-          if (i > 0) {
-            ok = wait(&bar_p_full[1], (uint32_t)(gs1 + i - 1) & 1u);
-            if (!ok) break;
-            issue_pv(1, st ^ 1, i > 1);
-            if (lane == 0) umma_commit(&bar_v_empty[st ^ 1]);
-          }
-          issue_s(1, st);
-        }
-        if (lane == 0) umma_commit(&bar_k_empty[st]);
-        ok = wait(&bar_v_full[st], par);
-        if (!ok) break;
-        ok = wait(&bar_p_full[0], (uint32_t)T & 1u);
-        if (!ok) break;
-        issue_pv(0, st, i > 0);
-        if (!two && lane == 0) umma_commit(&bar_v_empty[st]);
-      }
-      if (ok && two) {
-        ok = wait(&bar_p_full[1], (uint32_t)(gs1 + nt - 1) & 1u);
-        if (ok) {
-          issue_pv(1, (gt + nt - 1) & 1, nt > 1);
-          if (lane == 0) umma_commit(&bar_v_empty[(gt + nt - 1) & 1]);
-        }
-      }
-      if (lane == 0) umma_commit(&bar_o_done);
-      __syncwarp();
-    } else if (warp < 8) {
-      // ---- softmax: one thread a row ----
-      const int slot = warp >> 2, quad = warp & 3;
-      if (slot == 0 || two) {
-        const int r = tid;
-        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-        const uint32_t tSs = tmem + slot * kCKeys + lane_off, tOs = tmem + (2 + slot) * kCKeys + lane_off;
-        const bool rv = r < c.n_rows;
-        const int pi = c.i0 + (c.row0 + r) / a.G;          // the row's position
-        const int s_lo = c.i0 + (c.row0 + slot * kCRows) / a.G;  // the slot's first, and its last row's
-        const int s_hi = min(c.i_hi, c.i0 + (c.row0 + slot * kCRows + kCRows - 1) / a.G);
-        const int g0 = slot == 0 ? gt : gs1;
-        float M = -CUDART_INF_F, l = 0.f;
-        bool ok = true, poison = false;
-        for (int i = 0; i < nt; ++i) {
-          const int kt = c.key(u0 + i);
-          if (!__all_sync(0xffffffffu, c_wait(&bar_s_full[slot], (uint32_t)(g0 + i) & 1u, a, &s_abort))) { ok = false; break; }
-          tc_fence_after();
-          const CMeta& m = s_meta[(gt + i) & 3];
-          const bool whole = kt + kCKeys - 1 <= s_lo && (c.ret || kt + kCKeys - 1 < a.S || kt > s_hi - a.W) &&
-                             (m.there[0] & m.there[1] & m.there[2] & m.there[3]) == 0xffffffffu;
-          auto keep_word = [&](int w) {  // of positions [kt + 32 w, + 32), those that the row sees
-            const int base = kt + 32 * w;
+        const CMeta& m = s_meta[(gt + i) & 7];
+        const bool whole = kt + kCKeys - 1 <= s_lo && (c.ret || kt + kCKeys - 1 < a.S || kt > s_hi - a.W) &&
+                           (m.there[0] & m.there[1] & m.there[2] & m.there[3]) == 0xffffffffu;
+        if (!whole) {  // (the slot agrees) S of the positions that the row does not see becomes -inf
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            const int base = kt + 32 * x;
             const int nc = pi - base + 1;
             const uint32_t causal = !rv || nc <= 0 ? 0u : nc >= 32 ? 0xffffffffu : (1u << nc) - 1u;
             uint32_t near = 0xffffffffu;
@@ -529,133 +473,341 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
               near = (nsk <= 0 ? 0u : nsk >= 32 ? 0xffffffffu : (1u << nsk) - 1u) |
                      (nw <= 0 ? 0xffffffffu : nw >= 32 ? 0u : ~((1u << nw) - 1u));
             }
-            return causal & near & m.there[w];
-          };
-          // weights of 32 positions against `mm`, their packed fp16, the row's sum, and the largest logit
-          auto chunk = [&](int w, float mm, uint32_t (&pk)[16], float& ls, float& mx) {
+            const uint32_t bits = causal & near & m.there[x];
+            if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
             float v[32];
-            tmem_ld32(tSs + w * 32, v);
+            tmem_ld32(tSs + x * 32, v);
             tmem_wait_ld();
-            if (!whole) {
-              const uint32_t bits = keep_word(w);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1u ? v[e] : -CUDART_INF_F;
-            }
+            for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1u ? v[e] : -CUDART_INF_F;
+            tmem_st32(tSs + x * 32, v);
+          }
+          tmem_wait_st();
+        }
+        // ---- the weights against the running maximum, 32 columns at a time while the next
+        // are on their way, their fp16 over columns already read ----
+        auto weigh = [&](const float (&v)[32], int x) {
+          uint32_t pk[16];
+          float mx, sum;
+          auto form = [&]() {
+            const float base = kAqLift - (M == -CUDART_INF_F ? 0.f : M);
+            sum = 0.f;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float4 g = m.g[2 * w + q];
-              const float f = rs * g.x;
-              float t = v[16 * q];
-#pragma unroll
-              for (int e = 1; e < 15; e += 2) t = max3_nan(t, v[16 * q + e], v[16 * q + e + 1]);
-              t = max_nan(t, v[16 * q + 15]);
-              mx = max_nan(mx, fmaf(t, f, g.y));
-              const float add = g.y + kAqLift - mm;
+              const float4 g = m.g[2 * x + q];
+              const float fq = rs * g.x, add = g.y + base;
               float s0 = 0.f, s1 = 0.f;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 float x0 = v[16 * q + 2 * e], x1 = v[16 * q + 2 * e + 1];
-                fma2(x0, x1, f, add);
-                const float p0 = ex2f(x0), p1 = (e & 1) ? ex2_poly(x1) : ex2f(x1);
-                add2(s0, s1, p0, p1);
-                pk[8 * q + e] = pack_f16(p0, p1);
+                fma2(x0, x1, fq, add);
+                if ((e & 3) == 3) {  // one weight in four on the FMA pipe
+                  ex2_poly2(x0, x1);
+                } else {
+                  x0 = ex2f(x0);
+                  x1 = ex2f(x1);
+                }
+                add2(s0, s1, x0, x1);
+                pk[8 * q + e] = pack_f16(x0, x1);
               }
-              ls = fmaf(s0 + s1, g.z, ls);
+              sum = fmaf(s0 + s1, g.z, sum);
             }
           };
-          const float mspec = M == -CUDART_INF_F ? 0.f : M;
-          uint32_t pk[4][16];
-          float ls = 0.f, mx = -CUDART_INF_F;
+          form();
+          mx = -CUDART_INF_F;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) chunk(w, mspec, pk[w], ls, mx);
-          if (mx != mx) {  // a stored NaN that the row sees
-            poison = true;
-            mx = -CUDART_INF_F;
+          for (int q = 0; q < 2; ++q) {
+            const float* y = v + 16 * q;
+            float t0 = max3_nan(y[0], y[1], y[2]), t1 = max3_nan(y[3], y[4], y[5]);
+            t0 = max3_nan(t0, y[6], y[7]);
+            t1 = max3_nan(t1, y[8], y[9]);
+            t0 = max3_nan(t0, y[10], y[11]);
+            t1 = max3_nan(t1, y[12], y[13]);
+            t0 = max3_nan(t0, y[14], y[15]);
+            const float4 g = m.g[2 * x + q];
+            mx = max_nan(mx, fmaf(max_nan(t0, t1), rs * g.x, g.y));
           }
-          float mn = M, f = 1.f;
-          if (mx > M + kAqRescale || (M == -CUDART_INF_F && mx > M)) {
-            mn = mx;
-            f = M == -CUDART_INF_F ? 0.f : ex2f(M - mn);
-          }
-          if (__any_sync(0xffffffffu, mn != M)) {
+          poison = poison || mx != mx;  // a stored NaN that the row sees
+          const bool need = mx > M + kCRescale || (M == -CUDART_INF_F && mx > M);
+          if (__any_sync(0xffffffffu, need)) {
+            // rare after an item's first columns: the maximum moves, and with it O, l and the
+            // tile's weights so far
+            const float f = need ? (M == -CUDART_INF_F ? 0.f : ex2f(M - mx)) : 1.f;
+            M = need ? mx : M;
+            l *= f;
             // PV of the slot's previous tile has completed (S(i) was issued after it)
-            if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k) {
-                float o[32];
-                tmem_ld32(tOs + k * 32, o);
+            if (i > 0) {
+#pragma unroll 1
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t o[16];
+                tmem_ld16(tOs + k * 16, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) mul2(o[e], o[e + 1], f);
-                tmem_st32(tOs + k * 32, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(tOs + k * 16, o);
               }
             }
-            ls = 0.f;
-            float again = 0.f;
-            const float ms = mn == -CUDART_INF_F ? 0.f : mn;
+            tmem_wait_st();
+            const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+            for (int y = 0; y < x; ++y) {
+              uint32_t o[16];
+              tmem_ld16(tSs + y * 16, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int w = 0; w < 4; ++w) chunk(w, ms, pk[w], ls, again);
+              for (int e = 0; e < 16; ++e) {
+                const __half2 t = __hmul2(*reinterpret_cast<__half2*>(&o[e]), f2);
+                o[e] = *reinterpret_cast<const uint32_t*>(&t);
+              }
+              tmem_st16(tSs + y * 16, o);
+            }
+            form();
           }
-#pragma unroll
-          for (int w = 0; w < 4; ++w) tmem_st16(tSs + 16 * w, pk[w]);
-          M = mn;
-          l = fmaf(l, f, ls);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&bar_p_full[slot]);
-        }
-        if (ok && __all_sync(0xffffffffu, c_wait(&bar_o_done, seg_par, a, &s_abort))) {
-          tc_fence_after();
-          if (poison) l = CUDART_NAN_F;
-          const bool alone = u0 == 0 && nt == c.tiles;
-          const int tok = c.q0 + (c.row0 + r) / a.G, hq = h * a.G + (c.row0 + r) % a.G;
-          __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D;
-          const size_t prow = (size_t)(2 * blockIdx.x + (u0 > 0 ? 0 : 1)) * kCGroup + r;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            float o[32];
-            tmem_ld32(tOs + k * 32, o);
+          l += sum;
+          tmem_st16(tSs + 16 * x, pk);
+        };
+        {
+          float v0[32], v1[32];
+          tmem_ld32(tSs, v0);
+#pragma unroll 1
+          for (int x = 0; x < 4; x += 2) {
             tmem_wait_ld();
-            if (!rv) continue;
-            if (alone) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint4 v;
-                v.x = pack_bf16(o[e] * inv, o[e + 1] * inv);
-                v.y = pack_bf16(o[e + 2] * inv, o[e + 3] * inv);
-                v.z = pack_bf16(o[e + 4] * inv, o[e + 5] * inv);
-                v.w = pack_bf16(o[e + 6] * inv, o[e + 7] * inv);
-                *reinterpret_cast<uint4*>(orow + k * 32 + e) = v;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(a.cpart + prow * D + k * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
+            tmem_ld32(tSs + 32 * x + 32, v1);
+            weigh(v0, x);
+            tmem_wait_ld();
+            if (x == 0) tmem_ld32(tSs + 64, v0);
+            weigh(v1, x + 1);
           }
-          if (rv && !alone) *reinterpret_cast<float2*>(a.cpart_ml + prow * 2) = make_float2(M, l);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[slot]);
+      }
+      if (!ok || !c_wait(&bars.o_full[slot], seg & 1u, a, &s_abort)) { ok = false; break; }
+      tc_fence_after();
+      if (poison) l = CUDART_NAN_F;
+      const bool alone = w.u0 == 0 && w.nt == c.tiles;
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D;
+      const size_t prow = (size_t)(2 * blockIdx.x + (w.u0 > 0 ? 0 : 1)) * kCGroup + r;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {
+        float o[32];
+        tmem_ld32(tOs + k * 32, o);
+        tmem_wait_ld();
+        if (!rv) continue;
+        if (alone) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 u;
+            u.x = pack_bf16(o[e] * inv, o[e + 1] * inv);
+            u.y = pack_bf16(o[e + 2] * inv, o[e + 3] * inv);
+            u.z = pack_bf16(o[e + 4] * inv, o[e + 5] * inv);
+            u.w = pack_bf16(o[e + 6] * inv, o[e + 7] * inv);
+            *reinterpret_cast<uint4*>(orow + k * 32 + e) = u;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(a.cpart + prow * D + k * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
+      if (rv && !alone) *reinterpret_cast<float2*>(a.cpart_ml + prow * 2) = make_float2(M, l);
+      tc_fence_before();
+      mbar_arrive(&bars.o_empty[slot]);
+      ++seg;
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (s_abort) break;  // uniform
-    gt += nt;
-    if (two) gs1 += nt;
-    seg_par ^= 1u;
-    at += nt;
-    ++item;
+  } else if (warp < 12) {
+    // ---- K and V rows to fp16, swizzled ----
+    constexpr int LPR = D / 16;          // lanes a row (16 bytes each)
+    constexpr int RPI = 4 * (32 / LPR);  // rows the four warps take at once
+    const int r_lane = (warp - 8) * (32 / LPR) + lane / LPR, cl = lane % LPR;
+    // 16 dims are two 16-byte chunks of a 64-dim region; lanes of the two
+    // regions take them in opposite order, so eight lanes hit eight chunks
+    const int reg = cl >> 2, ch = (2 * cl) & 7, odd = reg & 1;
+    const int off0 = reg * kCRegion + r_lane * 128 + (((ch + odd) ^ (r_lane & 7)) << 4);
+    const int off1 = reg * kCRegion + r_lane * 128 + (((ch + 1 - odd) ^ (r_lane & 7)) << 4);
+    static_assert(RPI % 8 == 0, "a lane's rows share their swizzle");
+    auto convert = [&](const unsigned char* raw, unsigned char* dst, const CMeta& m, int n_valid, bool all) {
+#pragma unroll 4
+      for (int r = 0; r < kCKeys; r += RPI) {
+        uint4 x = *reinterpret_cast<const uint4*>(raw + (r + r_lane) * D + cl * 16);
+        // rows past the item's last position, or whose block is not there, hold anything: zeros
+        if (!all && (r + r_lane >= n_valid || !(m.there[(r + r_lane) >> 5] >> ((r + r_lane) & 31) & 1u)))
+          x = make_uint4(0u, 0u, 0u, 0u);
+        uint4 lo, hi;
+        e4m3x4_to_f16x4(x.x, lo.x, lo.y);
+        e4m3x4_to_f16x4(x.y, lo.z, lo.w);
+        e4m3x4_to_f16x4(x.z, hi.x, hi.y);
+        e4m3x4_to_f16x4(x.w, hi.z, hi.w);
+        *reinterpret_cast<uint4*>(dst + r * 128 + off0) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(dst + r * 128 + off1) = odd ? lo : hi;
+      }
+    };
+    CWalk w;
+    int T = 0;
+    bool ok = true;
+    for (bool more = w.start(a); more && ok; more = w.next(a)) {
+      for (int i = 0; i < w.nt; ++i, ++T) {
+        const int st = T & 1;
+        const uint32_t par = ((uint32_t)(T >> 1) & 1u) ^ 1u;
+        const CMeta& m = s_meta[T & 7];
+        const int n_valid = w.c.i_hi - tile_pos(w.c, w.u0 + i) + 1;
+        if (!(ok = c_wait(&bars.raw_full[0], (uint32_t)T & 1u, a, &s_abort))) break;
+        const bool all = n_valid >= kCKeys && (m.there[0] & m.there[1] & m.there[2] & m.there[3]) == 0xffffffffu;
+        if (!(ok = c_wait(&bars.k_empty[st], par, a, &s_abort))) break;
+        convert(dsm + SM::kOffRaw, dsm + SM::kOffK + st * SM::kOp, m, n_valid, all);
+        fence_async_smem();
+        mbar_arrive(&bars.raw_empty[0]);
+        mbar_arrive(&bars.k_full[st]);
+        if (!(ok = c_wait(&bars.raw_full[1], (uint32_t)T & 1u, a, &s_abort))) break;
+        if (!(ok = c_wait(&bars.v_empty[st], par, a, &s_abort))) break;
+        convert(dsm + SM::kOffRaw + SM::kRaw, dsm + SM::kOffV + st * SM::kOp, m, n_valid, all);
+        fence_async_smem();
+        mbar_arrive(&bars.raw_empty[1]);
+        mbar_arrive(&bars.v_full[st]);
+      }
+    }
+  } else {
+    if (warp == 12) {
+      // ---- the products ----
+      constexpr uint32_t idS = umma_idesc(kCRows, kCKeys, false, true);
+      constexpr uint32_t idO = umma_idesc(kCRows, D, true, true);
+      const uint64_t dq0 = umma_desc(smem_u32(dsm + SM::kOffQ), 16, 1024), dk0 = umma_desc(smem_u32(dsm + SM::kOffK), 16, 1024);
+      const uint64_t dv0 = umma_desc(smem_u32(dsm + SM::kOffV), kCRegion, 1024);
+      const uint32_t lead = elect_lane();
+      auto uni = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };  // a value that the warp agrees on
+      const uint32_t tm = uni(tmem);
+      auto issue_s = [&](int slot, int stage) {
+        const uint64_t dq = dq0 + (uint64_t)((slot * SM::kOp) >> 4), dk = dk0 + (uint64_t)uni((stage * SM::kOp) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (uint32_t)(((kk / 4) * kCRegion + (kk % 4) * 32) >> 4);
+          umma_f16_by(lead, tm + slot * kCKeys, dq + off, dk + off, idS, kk > 0 ? 1u : 0u);
+        }
+        mbar_arrive_by(lead, &bars.s_full[slot]);
+        umma_commit_by(lead, &bars.s_full[slot]);
+      };
+      auto issue_pv = [&](int slot, int stage, bool acc) {
+        const uint64_t dv = dv0 + (uint64_t)uni((stage * SM::kOp) >> 4);
+        const uint32_t ac = uni(acc ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < kCKeys / 16; ++kk)
+          umma_f16_ts_by(lead, tm + (2 + slot) * kCKeys, tm + slot * kCKeys + kk * 8, dv + (uint64_t)((kk * 2048) >> 4),
+                         idO, kk > 0 ? 1u : ac);
+      };
+      auto commit = [&](uint64_t* bar) { umma_commit_by(lead, bar); };
+      auto wait = [&](uint64_t* bar, uint32_t par) { return c_wait(bar, par, a, &s_abort); };
+      auto wait_tmem = [&](uint64_t* bar, uint32_t par) {  // for what other warps did to TMEM
+        const bool ok = c_wait(bar, par, a, &s_abort);
+        tc_fence_after();
+        return ok;
+      };
+      int T = 0;
+      uint32_t seg0 = 0u, seg1 = 0u, ph1 = 0u;  // items of each slot; phase of slot 1's weights
+      bool owed = false, owed_first = false, owed_last = false;  // PV1 of the tile before is still to issue
+      auto pay = [&]() {  // PV1 of tile T - 1
+        if (!wait_tmem(&bars.p_full[1], ph1)) return false;
+        if (owed_first && !wait_tmem(&bars.o_empty[1], (seg1 & 1u) ^ 1u)) return false;  // the last item's O has been read
+        ph1 ^= 1u;
+        issue_pv(1, (T - 1) & 1, !owed_first);
+        commit(&bars.v_empty[(T - 1) & 1]);
+        if (owed_last) {
+          commit(&bars.o_full[1]);
+          ++seg1;
+        }
+        owed = false;
+        return true;
+      };
+      CWalk w;
+      bool ok = true;
+      for (bool more = w.start(a); more && ok; more = w.next(a)) {
+        uint32_t q1 = 0u;
+        for (int i = 0; i < w.nt; ++i, ++T) {
+          const int st = T & 1;
+          const uint32_t par = (uint32_t)(T >> 1) & 1u;
+          const bool first = i == 0, last = i + 1 == w.nt;
+          if (first && !(ok = wait(&bars.q_full[0], seg0 & 1u))) break;
+          if (!(ok = wait(&bars.k_full[st], par))) break;
+          issue_s(0, st);
+          if (last) commit(&bars.q_empty[0]);
+          if (owed && !(ok = pay())) break;
+          if (w.two) {
+            if (first) {
+              q1 = seg1 & 1u;
+              if (!(ok = wait(&bars.q_full[1], q1))) break;
+            }
+            issue_s(1, st);
+            if (last) commit(&bars.q_empty[1]);
+          }
+          commit(&bars.k_empty[st]);
+          if (!(ok = wait(&bars.v_full[st], par))) break;
+          if (!(ok = wait_tmem(&bars.p_full[0], (uint32_t)T & 1u))) break;
+          if (first && !(ok = wait_tmem(&bars.o_empty[0], (seg0 & 1u) ^ 1u))) break;
+          issue_pv(0, st, !first);
+          if (last) {
+            commit(&bars.o_full[0]);
+            ++seg0;
+          }
+          if (w.two) {
+            owed = true;
+            owed_first = first;
+            owed_last = last;
+          } else {
+            commit(&bars.v_empty[st]);
+          }
+        }
+      }
+      if (ok && owed) pay();
+      // every product issued has completed before TMEM is freed
+      commit(&bars.fin);
+      mbar_wait_bounded(&bars.fin, 0u, a.wait_ns, a.pool.status);
+    } else if (warp == 13) {
+      // ---- loads: Q (128 rows of a slot are 128 / G tokens of the group's G
+      // heads), then the tiles' rows from their blocks ----
+      CWalk w;
+      uint32_t nq[2] = {0u, 0u}, nr[2] = {0u, 0u};  // loads so far: each slot's Q; K rows and V rows
+      int T = 0, flags = 0;
+      bool ok = true;
+      for (bool more = w.start(a); more && ok; more = w.next(a)) {
+        for (int i = 0; i < w.nt && ok; ++i, ++T) {
+          // lane g < 8: the block of positions [16 g, 16 g + 16) of the tile; -1: there is none
+          int id = -1;
+          const int j = tile_pos(w.c, w.u0 + i) + 16 * (lane & 7);
+          if (j <= w.c.i_hi) {
+            id = a.c.block_table[(size_t)w.c.b * a.pool.table_cols + (j >> a.pool.log_bs)];
+            if ((unsigned)id >= (unsigned)a.pool.n_blocks) {
+              flags |= RTP_DEV_BLOCKS;
+              id = -1;
+            }
+          }
+          ok = load_rows_of_tile<D>(a, w, T, id, bars, dsm + SM::kOffRaw, s_meta, &s_abort, nr);
+          if (i > 0) continue;
+          for (int slot = 0; slot < (w.two ? 2 : 1) && ok; ++slot) {
+            if (!(ok = c_wait(&bars.q_empty[slot], (nq[slot] & 1u) ^ 1u, a, &s_abort))) break;
+            if (lane == 0) {
+              mbar_expect_tx(&bars.q_full[slot], (uint32_t)SM::kOp);
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_3d(dsm + SM::kOffQ + slot * SM::kOp + x * kCRegion, &a.tm_q, x * 64, w.c.h * a.G,
+                            w.c.q0 + ((w.c.row0 + slot * kCRows) >> a.log_g), &bars.q_full[slot]);
+            }
+            __syncwarp();
+            ++nq[slot];
+          }
+        }
+      }
+      if (flags) atomicOr(a.pool.status, flags);
+      // where the CTA gave up, its copies land before it leaves
+      for (int x = 0; x < 2; ++x) {
+        if (nq[x] > 0) mbar_wait_bounded(&bars.q_full[x], (nq[x] - 1u) & 1u, a.wait_ns, a.pool.status);
+        if (nr[x] > 0) mbar_wait_bounded(&bars.raw_full[x], (nr[x] - 1u) & 1u, a.wait_ns, a.pool.status);
+      }
+    }
   }
-  if (flags) atomicOr(a.pool.status, flags);
-  // every product issued has completed before TMEM is freed
+  tc_fence_before();
+  __syncthreads();
   if (warp == 12) {
-    if (lane == 0) {
-      umma_commit(&bar_fin);
-      mbar_wait_bounded(&bar_fin, 0u, a.wait_ns, a.pool.status);
-    }
-    __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kCTmemCols) : "memory");
   }
@@ -668,7 +820,7 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
   constexpr int LPR = D / 4;  // threads a row
   griddep_wait();
   const int n_items = a.req_items[a.B];
-  const long long total = a.prefix[n_items], share = chunk_share(total);
+  const long long total = a.prefix[n_items], share = a.prefix[a.max_chunk_items + 1];
   const int cut = blockIdx.x + 1;
   const long long at = cut * share;
   if (at >= total) return;
@@ -676,9 +828,7 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
   const long long first = a.prefix[item];
   if (first == at || at - share > first) return;  // between two items, or not the item's first cut
   const int c1 = (int)((a.prefix[item + 1] - 1) / share);
-  const ChunkItem ci = a.items[item];
-  int dummy = 0;
-  const CItem c = chunk_item(a, load_rows(a, ci.b, dummy), ci.h, ci.grp);
+  const ChunkItem c = a.items[item];
   const int r = blockIdx.y * (256 / LPR) + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
   if (r >= c.n_rows) return;
   // the share that starts the item keeps its partial second, the later ones first
@@ -699,7 +849,7 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
     o.z = fmaf(p.z, f, o.z);
     o.w = fmaf(p.w, f, o.w);
   }
-  const int tok = c.q0 + (c.row0 + r) / a.G, hq = ci.h * a.G + (c.row0 + r) % a.G;
+  const int tok = c.q0 + ((c.row0 + r) >> a.log_g), hq = c.h * a.G + ((c.row0 + r) & (a.G - 1));
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2 v;
   v.x = pack_bf16(o.x * inv, o.y * inv);
@@ -718,17 +868,19 @@ long long max_chunk_items(const Shape& sh, int n_tokens, int max_q, int small) {
 }
 
 struct ChunkLayout {
-  size_t prefix, items, reqs, part, ml, total;
+  size_t prefix, items, reqs, part, ml, q, unit, total;
 };
-ChunkLayout chunk_layout(const Shape& sh, long long items) {
+ChunkLayout chunk_layout(const Shape& sh, int n_tokens, long long items) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   ChunkLayout l;
   l.prefix = 0;
-  l.items = up((size_t)(items + 1) * sizeof(long long));
+  l.items = up((size_t)(items + 2) * sizeof(long long));
   l.reqs = l.items + up((size_t)items * sizeof(ChunkItem));
   l.part = l.reqs + up((size_t)(sh.B + 1) * sizeof(int));
   l.ml = l.part + (size_t)2 * kCCtas * kCGroup * sh.D * sizeof(float);
-  l.total = l.ml + up((size_t)2 * kCCtas * kCGroup * 2 * sizeof(float));
+  l.q = l.ml + up((size_t)2 * kCCtas * kCGroup * 2 * sizeof(float));
+  l.unit = l.q + up((size_t)n_tokens * sh.Hq * sh.D * sizeof(__half));
+  l.total = l.unit + up((size_t)n_tokens * sh.Hq * sizeof(float));
   return l;
 }
 
@@ -747,7 +899,8 @@ cudaError_t launch_chunks(const AttnQ8Args& a, cudaStream_t st) {
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  e = launch_pdl(chunk_line_kernel, dim3(1), dim3(1024), 0, st, a);
+  const long long tasks = (long long)a.c.n_tokens * ((a.Hq + 7) / 8);
+  e = launch_pdl(chunk_prep_kernel<D>, dim3((unsigned)(1 + (tasks + kCPrep / 32 - 1) / (kCPrep / 32))), dim3(kCPrep), 0, st, a);
   if (e == cudaSuccess) e = launch_pdl(attn_q8_chunk_kernel<D>, dim3(kCCtas), dim3(kCThreads), CSmem<D>::kBytes, st, a);
   if (e == cudaSuccess)
     e = launch_pdl(attn_q8_chunk_join_kernel<D>, dim3(kCCtas - 1, kCGroup * (D / 4) / 256), dim3(256), 0, st, a);
@@ -757,12 +910,19 @@ cudaError_t launch_chunks(const AttnQ8Args& a, cudaStream_t st) {
 }  // namespace
 
 size_t chunk_workspace_bytes(const Shape& sh, int n_tokens, int max_q, int small_rows) {
-  return chunk_layout(sh, max_chunk_items(sh, n_tokens, max_q, small_rows)).total;
+  return chunk_layout(sh, n_tokens, max_chunk_items(sh, n_tokens, max_q, small_rows)).total;
 }
 
-void chunk_carve(const Shape& sh, int n_tokens, int max_q, int small_rows, void* ws, AttnQ8Args* a) {
+bool chunk_carve(const Shape& sh, int n_tokens, int max_q, int small_rows, void* ws, AttnQ8Args* a) {
+  const unsigned long long rows = ((unsigned long long)a->pool.n_blocks * sh.Hkv) << a->pool.log_bs;
+  const unsigned box_rows = 1u << a->pool.log_bs;
+  if (!make_tensor_map(&a->tm_ck, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->pool.k, sh.D, rows, sh.D, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !make_tensor_map(&a->tm_cv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->pool.v, sh.D, rows, sh.D, box_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return false;
   const long long items = max_chunk_items(sh, n_tokens, max_q, small_rows);
-  const ChunkLayout l = chunk_layout(sh, items);
+  const ChunkLayout l = chunk_layout(sh, n_tokens, items);
   unsigned char* p = static_cast<unsigned char*>(ws);
   a->prefix = reinterpret_cast<long long*>(p + l.prefix);
   a->items = reinterpret_cast<ChunkItem*>(p + l.items);
@@ -770,6 +930,17 @@ void chunk_carve(const Shape& sh, int n_tokens, int max_q, int small_rows, void*
   a->cpart = reinterpret_cast<float*>(p + l.part);
   a->cpart_ml = reinterpret_cast<float*>(p + l.ml);
   a->max_chunk_items = (int)items;
+  a->cq = reinterpret_cast<__half*>(p + l.q);
+  a->cq_unit = reinterpret_cast<float*>(p + l.unit);
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)sh.D, (cuuint64_t)sh.Hq, (cuuint64_t)n_tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)sh.D * 2, (cuuint64_t)sh.Hq * sh.D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)sh.G, (cuuint32_t)(kCRows / sh.G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(&a->tm_q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, a->cq, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_attn_q8_chunks(const Shape& sh, const AttnQ8Args& a, cudaStream_t st) {

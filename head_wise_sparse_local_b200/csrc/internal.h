@@ -51,6 +51,7 @@ struct Shape {
   int ret_head[64];  // rank -> kv head
   int ret_rank[64];  // kv head -> rank or -1
   double inv_freq[64];  // RoPE frequencies base^(-2k/D), k < D/2, fp64 on the host
+  uint64_t turns[64];   // the same in turns, inv_freq / (2 pi), as 0.64 fixed point
 };
 
 // Validates cfg and fills Shape; returns RTP_OK or an error (message set).

@@ -10,11 +10,10 @@ namespace rtp {
 
 constexpr float kQ8ScaleMin = 5.42101086242752217e-20f;  // 2^-64, the smallest block scale
 
-// Two e4m3 values (low byte first) as fp16, exactly; the upper half of `two` is ignored.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-  return r;
+// Four e4m3 values (low byte first) as two fp16 pairs, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
 // Nearest e4m3 values (ties to even) of two floats, lo in the low byte.
@@ -35,5 +34,13 @@ __device__ __forceinline__ float q8_scale(float a) {
 
 // 1 / s of a power of two 2^-64 <= s <= 2^121, exactly.
 __device__ __forceinline__ float q8_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+// cos and sin of a rotary angle from its frequency in turns (0.64 fixed
+// point): the product with the position wraps around modulo one turn, so no
+// position is too far for the reduction, and what is left goes to fp32 once.
+__device__ __forceinline__ void rope_turns(int pos, uint64_t turns, float& c, float& s) {
+  const long long frac = (long long)((uint64_t)(long long)pos * turns);  // [-1/2, 1/2) turn, times 2^64
+  sincospif(__ll2float_rn(frac) * 1.0842021724855044e-19f, &s, &c);     // half turns: 2^-63
+}
 
 }  // namespace rtp

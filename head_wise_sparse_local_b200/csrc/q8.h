@@ -46,6 +46,7 @@ struct AttnQ8Call {
   void* out;
 };
 size_t attn_q8_workspace_bytes(const Shape& sh, int n_tokens, int max_q);
+bool attn_q8_fits(const Shape& sh, int max_q, int max_seq_len);
 int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, const AttnQ8Call& c, void* ws,
                    cudaStream_t st);
 

@@ -119,14 +119,18 @@ int make_shape(const rtp_layer_cfg* cfg, Shape* sh) {
     float base = 0.0f;
     int D = 0;
     double f[64];
+    uint64_t turns[64];
   } freq;
   if (freq.base != sh->rope_base || freq.D != sh->D) {
     for (int k = 0; k < 64; ++k)
       freq.f[k] = k < sh->D / 2 ? std::pow((double)sh->rope_base, -2.0 * k / (double)sh->D) : 0.0;
+    for (int k = 0; k < 64; ++k)
+      freq.turns[k] = (uint64_t)std::llroundl((long double)freq.f[k] / 6.283185307179586476925286766559L * 9223372036854775808.0L) << 1;
     freq.base = sh->rope_base;
     freq.D = sh->D;
   }
   std::memcpy(sh->inv_freq, freq.f, sizeof(freq.f));
+  std::memcpy(sh->turns, freq.turns, sizeof(freq.turns));
   return RTP_OK;
 }
 
