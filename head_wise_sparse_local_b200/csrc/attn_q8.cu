@@ -14,7 +14,10 @@
 // tiles of all items form one line that is cut into equal shares, one for
 // each CTA (two an SM), so ragged batches and the short local heads load the
 // SMs evenly; an item that a cut goes through leaves one partial (O, M, l) a
-// CTA, and a second kernel joins them in order.  Inside a CTA each of 4 warps
+// CTA, and a second kernel joins them in order, from a note that the item's
+// first CTA leaves it (finding the items anew cost it 4 us at 128K; a join by
+// the CTA that arrives last, counted by compare-and-swap so that the workspace
+// needs no clearing, 30 us for 70 CTAs an item).  Inside a CTA each of 4 warps
 // takes every fourth tile and keeps its own softmax state and accumulators;
 // they meet once an item.
 //
@@ -182,7 +185,7 @@ struct AqSmem {
   static constexpr int kOffQ = kRing;                                  // rotated queries, fp32
   static constexpr int kOffMeta = kOffQ + ROWS * kQPitch * 4;
   static constexpr int kBytes = kOffMeta + kAqWarps * kAqStages * (int)sizeof(TileMeta) + 1024;
-  static constexpr int kMPitch = D + 2;                                // joining the warps: O rows, M, l (over the ring)
+  static constexpr int kMPitch = D + 4;                                // joining the warps: O rows, M, l (over the ring)
   static_assert(kAqWarps * ROWS * kMPitch * 4 <= kRing, "the warps' partials fit in the ring");
 };
 
@@ -220,7 +223,11 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
   LineAt line = locate(a, blockIdx.x, flags);
   if (blockIdx.x == 0 && warp == 0 && flags) atomicOr(a.pool.status, flags);
   flags = 0;
-  if (line.b < 0) return;  // uniform
+  JoinJob job = {};
+  if (line.b < 0) {  // uniform
+    if (tid == 0) a.jobs[blockIdx.x] = job;
+    return;
+  }
   uint32_t at = line.at;
   const uint32_t end = min(line.total, at + line.share);
   int b = line.b;
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     const int i0 = rq.L - rq.n;                            // position of the request's first query
     const int i_lo = i0 + (row0 >> a.log_g), i_hi = i0 + ((row0 + n_rows - 1) >> a.log_g);  // of this chunk's rows
     const int* tab = a.c.block_table + (size_t)b * a.pool.table_cols;
-    const int mine = u0 + warp < u1 ? (u1 - u0 - warp + kAqWarps - 1) / kAqWarps : 0;  // this warp's tiles
+    const int mine = u0 + warp < u1 && !s_abort ? (u1 - u0 - warp + kAqWarps - 1) / kAqWarps : 0;  // this warp's tiles
 
     auto tile_key = [&](int n) {  // first position of the warp's n-th tile
       const int u = u0 + warp + n * kAqWarps;
@@ -291,6 +298,32 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
       tma_tile(dst + kAqTile * D, &a.tm_v, y[0], &bar[s], pol);
       if (split) tma_tile(dst + kAqTile * D + 16 * D, &a.tm_v, y[1], &bar[s], pol);
     };
+    // ---- queries: asked for before the stream's copies, which fill the memory system for
+    // microseconds; a thread turns a rotary pair of all the chunk's rows of one token ----
+    const int tok0 = row0 >> a.log_g, n_tok = ((row0 + n_rows - 1) >> a.log_g) - tok0 + 1;
+    struct Pair {
+      uint64_t turns;
+      int pos, ra, rb;     // rows [ra, rb) of the chunk
+      float x1[8], x2[8];  // a token has at most 8 rows
+    };
+    auto load_pair = [&](int task, Pair& y) {
+      const int tl = task / (D / 2), k = task % (D / 2), tok = rq.q0 + tok0 + tl;
+      y.turns = table_at(a.turns, k);
+      y.pos = a.c.pos[(size_t)(a.rope.n_axes > 1 ? table_at(a.rope.axis, k) : 0) * a.c.n_tokens + tok];
+      y.ra = max(((tok0 + tl) << a.log_g) - row0, 0);
+      y.rb = min(((tok0 + tl + 1) << a.log_g) - row0, n_rows);
+      const T* q = static_cast<const T*>(a.c.q_pre) + (size_t)tok * a.c.q_stride +
+                   (size_t)(h * a.G + ((row0 + y.ra) & (a.G - 1))) * D + k;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (y.ra + r < y.rb) {
+          y.x1[r] = to_f32(q[(size_t)r * D]);
+          y.x2[r] = to_f32(q[(size_t)r * D + D / 2]);
+        }
+    };
+    Pair pair;
+    if (tid < n_tok * (D / 2)) load_pair(tid, pair);
+
     // the first tiles, a lane each, so that their block numbers are read at once
     if (lane < kAqStages && lane < mine) {
       int id[2], s = st + lane;
@@ -300,29 +333,17 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     int next_id[2] = {0, 0};  // blocks of the next tile to issue
     if (lane == 0 && mine > kAqStages) block_ids(kAqStages, next_id);
 
-    // ---- queries: rotated in fp32, then as fp16 operands of a power-of-two scale a row ----
-    // (a thread turns a rotary pair of all the chunk's rows of one token)
-    const int tok0 = row0 >> a.log_g, n_tok = ((row0 + n_rows - 1) >> a.log_g) - tok0 + 1;
+    // ---- rotated in fp32, then fp16 operands of a power-of-two scale a row ----
     for (int task = tid; task < n_tok * (D / 2); task += kAqThreads) {
-      const int tl = task / (D / 2), k = task % (D / 2), tok = rq.q0 + tok0 + tl;
-      const int p = a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + tok];
-      const int ra = max(((tok0 + tl) << a.log_g) - row0, 0), rb = min(((tok0 + tl + 1) << a.log_g) - row0, n_rows);
-      const T* q = static_cast<const T*>(a.c.q_pre) + (size_t)tok * a.c.q_stride +
-                   (size_t)(h * a.G + ((row0 + ra) & (a.G - 1))) * D + k;
-      float x1[8], x2[8];  // a token has at most 8 rows
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (ra + r < rb) {
-          x1[r] = to_f32(q[(size_t)r * D]);
-          x2[r] = to_f32(q[(size_t)r * D + D / 2]);
-        }
+      if (task != tid) load_pair(task, pair);
+      const int k = task % (D / 2);
       float c, s;
-      rope_turns(p, a.turns[k], c, s);
+      rope_turns(pair.pos, pair.turns, c, s);
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (ra + r < rb) {
-          s_q[(ra + r) * SM::kQPitch + k] = x1[r] * c - x2[r] * s;
-          s_q[(ra + r) * SM::kQPitch + k + D / 2] = x2[r] * c + x1[r] * s;
+        if (pair.ra + r < pair.rb) {
+          s_q[(pair.ra + r) * SM::kQPitch + k] = pair.x1[r] * c - pair.x2[r] * s;
+          s_q[(pair.ra + r) * SM::kQPitch + k + D / 2] = pair.x2[r] * c + pair.x1[r] * s;
         }
     }
     for (int i = n_rows * D + tid; i < ROWS * D; i += kAqThreads) s_q[(i / D) * SM::kQPitch + i % D] = 0.f;
@@ -544,7 +565,6 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     }
     // ---- join the warps (their partials over the ring, once every warp is done with it) ----
     __syncthreads();
-    if (s_abort) break;  // uniform
     float* mg = reinterpret_cast<float*>(dsm);
     {
       float* mw = mg + warp * ROWS * SM::kMPitch;
@@ -566,102 +586,131 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     __syncthreads();
     const bool alone = u0 == 0 && u1 == nt;  // the whole item is here
     const uint32_t slot = blockIdx.x + item;
-    for (int i = tid; i < n_rows * D; i += kAqThreads) {
-      const int r = i / D, d = i % D;
+    auto write_out = [&](int r, int d, const float4& o, float l) {
+      const int tok = rq.q0 + ((row0 + r) >> a.log_g), hq = h * a.G + ((row0 + r) & (a.G - 1));
+      T* p = static_cast<T*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D + d;
+      const T y[4] = {finish<T>(o.x, l), finish<T>(o.y, l), finish<T>(o.z, l), finish<T>(o.w, l)};
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(y);
+      else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(y);
+    };
+    for (int i = tid; i < n_rows * (D / 4); i += kAqThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
       const float* p = mg + r * SM::kMPitch;
-      float m = -CUDART_INF_F;
+      constexpr int kW = ROWS * SM::kMPitch;  // between warps
+      float m = p[D];
 #pragma unroll
-      for (int w = 0; w < kAqWarps; ++w) m = fmaxf(m, p[w * ROWS * SM::kMPitch + D]);
+      for (int w = 1; w < kAqWarps; ++w) m = fmaxf(m, p[w * kW + D]);
       const float ms = m == -CUDART_INF_F ? 0.f : m;
-      float os = 0.f, ls = 0.f;
+      float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
 #pragma unroll
       for (int w = 0; w < kAqWarps; ++w) {
-        const float f = ex2(p[w * ROWS * SM::kMPitch + D] - ms);
-        os = fmaf(p[w * ROWS * SM::kMPitch + d], f, os);
-        ls = fmaf(p[w * ROWS * SM::kMPitch + D + 1], f, ls);
+        const float f = ex2(p[w * kW + D] - ms);
+        const float4 v = *reinterpret_cast<const float4*>(p + w * kW + d);
+        os.x = fmaf(v.x, f, os.x);
+        os.y = fmaf(v.y, f, os.y);
+        os.z = fmaf(v.z, f, os.z);
+        os.w = fmaf(v.w, f, os.w);
+        ls = fmaf(p[w * kW + D + 1], f, ls);
       }
       if (alone) {
-        const int tok = rq.q0 + ((row0 + r) >> a.log_g), hq = h * a.G + ((row0 + r) & (a.G - 1));
-        static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + d] = finish<T>(os, ls);
+        write_out(r, d, os, ls);
       } else if (slot < a.n_slots) {  // always, unless cu_q goes back and forth
-        a.part[((size_t)slot * ROWS + r) * D + d] = os;
-        if (d == 0) {
-          a.part_ml[((size_t)slot * ROWS + r) * 2] = m;
-          a.part_ml[((size_t)slot * ROWS + r) * 2 + 1] = ls;
-        }
+        *reinterpret_cast<float4*>(a.part + ((size_t)slot * ROWS + r) * D + d) = os;
+        if (d == 0) *reinterpret_cast<float2*>(a.part_ml + ((size_t)slot * ROWS + r) * 2) = make_float2(m, ls);
       }
+    }
+    if (u0 == 0 && u1 < nt) {  // the cut behind this CTA is the item's first
+      job.np = (int)((at + (uint32_t)nt - 1) / line.share - blockIdx.x) + 1;
+      job.n_rows = slot + (uint32_t)job.np <= a.n_slots ? n_rows : 0;
+      job.slot0 = slot;
+      job.h = h;
+      job.row0 = row0;
+      job.q0 = rq.q0;
     }
     fence_async_smem();  // the ring held ordinary stores; the next segment's copies overwrite them
     __syncthreads();
     at += u1 - u0;
   }
+  if (tid == 0) a.jobs[blockIdx.x] = job;
   if (flags) atomicOr(a.pool.status, flags);
 }
 
-// Joins the partials of the items that cuts of the line go through.  CTA column
-// x stands for the cut ahead of share x + 1 and works if that is its item's
-// first; a CTA takes one row, its warps the partials in turn.
+// Joins the partials of an item (x: the CTA whose note it is) for one row (y):
+// a lane a partial for the weights, then the warps the partials in turn.
 constexpr int kAqJoinWarps = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kAqJoinWarps * 32) attn_q8_join_kernel(const __grid_constant__ AttnQ8Args a) {
   constexpr int E = D / 32;  // dims a lane
-  __shared__ float s_o[kAqJoinWarps][D], s_m[kAqJoinWarps], s_l[kAqJoinWarps];
+  __shared__ float s_o[kAqJoinWarps][D], s_f[kAqMaxCtas], s_l[kAqJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
-  // Everything up to the partials was there before the streaming kernel started.
-  int flags = 0;
-  const uint32_t cut = blockIdx.x + 1;
-  const LineAt line = locate(a, cut, flags);
   griddep_wait();
-  if (line.b < 0) return;
-  const ReqQ8 rq = load_req(a, line.b, flags);
-  uint32_t rel = line.at - line.tiles;
-  const ItemAt x = item_at(a, rq, rel);
-  const int row = x.rch * a.rows + r;
-  if (rel == 0 || rel > line.share || row >= rq.n * a.G) return;  // between items, or not the first cut of its item
-  const uint32_t first = line.at - rel;  // the item's first tile on the line
-  const int np = (int)((first + (uint32_t)x.nt - 1) / line.share - (cut - 1)) + 1;  // CTAs cut - 1 and on
-  const size_t slot = (size_t)(cut - 1) + line.items + (uint32_t)(x.h * rq.rc + x.rch);
-  const float* ml = a.part_ml + (slot * a.rows + r) * 2;
-  const float* po = a.part + (slot * a.rows + r) * D + lane * E;
-  float m = -CUDART_INF_F, l = 0.f, o[E];
+  const JoinJob job = a.jobs[blockIdx.x];
+  if (job.np == 0 || r >= job.n_rows) return;
+  const float* ml = a.part_ml + ((size_t)job.slot0 * a.rows + r) * 2;
+  const float* po = a.part + ((size_t)job.slot0 * a.rows + r) * D + lane * E;
+  // the first partials of each warp are on their way before their weights are known
+  constexpr int kFirst = 8;
+  float2 v[kFirst][E / 2];
+#pragma unroll
+  for (int k = 0; k < kFirst; ++k)
+    if (warp + k * kAqJoinWarps < job.np) {
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e)
+        v[k][e] = reinterpret_cast<const float2*>(po + (size_t)(warp + k * kAqJoinWarps) * a.rows * D)[e];
+    }
+  float m = -CUDART_INF_F;
+  for (int p = lane; p < job.np; p += 32) m = fmaxf(m, ml[(size_t)p * a.rows * 2]);
+  m = warp_max(m);
+  const float ms = m == -CUDART_INF_F ? 0.f : m;
+  float l = 0.f;
+  for (int p = tid; p < job.np; p += kAqJoinWarps * 32) {
+    const float2 y = *reinterpret_cast<const float2*>(ml + (size_t)p * a.rows * 2);
+    const float f = ex2(y.x - ms);
+    s_f[p] = f;
+    l = fmaf(y.y, f, l);
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < kFirst; ++k)
+    if (warp + k * kAqJoinWarps < job.np) {
+      const float f = s_f[warp + k * kAqJoinWarps];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        o[2 * e] = fmaf(v[k][e].x, f, o[2 * e]);
+        o[2 * e + 1] = fmaf(v[k][e].y, f, o[2 * e + 1]);
+      }
+    }
 #pragma unroll 4
-  for (int p = warp; p < np; p += kAqJoinWarps) {
-    const float2 y = *reinterpret_cast<const float2*>(ml + (size_t)p * a.rows * 2);
-    float v[E];
+  for (int p = warp + kFirst * kAqJoinWarps; p < job.np; p += kAqJoinWarps) {
+    const float f = s_f[p];
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<float2*>(v + e) = *reinterpret_cast<const float2*>(po + (size_t)p * a.rows * D + e);
-    const float mn = fmaxf(m, y.x);
-    const float f0 = m == -CUDART_INF_F ? 0.f : ex2(m - mn), f1 = mn == -CUDART_INF_F ? 1.f : ex2(y.x - mn);
-    m = mn;
-    l = l * f0 + y.y * f1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f0 + v[e] * f1;
+    for (int e = 0; e < E; e += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(po + (size_t)p * a.rows * D + e);
+      o[e] = fmaf(y.x, f, o[e]);
+      o[e + 1] = fmaf(y.y, f, o[e + 1]);
+    }
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
   __syncthreads();
   if (tid >= D) return;
-#pragma unroll
-  for (int w = 0; w < kAqJoinWarps; ++w) m = fmaxf(m, s_m[w]);
-  const float ms = m == -CUDART_INF_F ? 0.f : m;
-  float os = 0.f;
-  l = 0.f;
+  float os = 0.f, ls = 0.f;
 #pragma unroll
   for (int w = 0; w < kAqJoinWarps; ++w) {
-    const float f = ex2(s_m[w] - ms);
-    os = fmaf(s_o[w][tid], f, os);
-    l = fmaf(s_l[w], f, l);
+    os += s_o[w][tid];
+    ls += s_l[w];
   }
-  const int tok = rq.q0 + (row >> a.log_g), hq = x.h * a.G + (row & (a.G - 1));
-  static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + tid] = finish<T>(os, l);
+  const int row = job.row0 + r;
+  const int tok = job.q0 + (row >> a.log_g), hq = job.h * a.G + (row & (a.G - 1));
+  static_cast<T*>(a.c.out)[((size_t)tok * a.Hq + hq) * D + tid] = finish<T>(os, ls);
 }
 
 // Requests of up to this many query rows a KV head (n G) are streamed, larger
@@ -697,7 +746,7 @@ long long max_items(const Shape& sh, int n_tokens, int max_q) {
 }
 
 template <typename T, int D, int ROWS>
-cudaError_t launch(const AttnQ8Args& a, cudaStream_t st) {
+cudaError_t launch(const AttnQ8Args& a, int most_rows, cudaStream_t st) {
   static std::mutex mu;
   static bool done[64] = {};
   int dev = 0;
@@ -714,7 +763,8 @@ cudaError_t launch(const AttnQ8Args& a, cudaStream_t st) {
   }
   e = launch_pdl(attn_q8_kernel<T, D, ROWS>, dim3(kAqMaxCtas), dim3(kAqThreads), smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_q8_join_kernel<T, D>, dim3(kAqMaxCtas - 1, ROWS), dim3(kAqJoinWarps * 32), 0, st, a);
+  return launch_pdl(attn_q8_join_kernel<T, D>, dim3(kAqMaxCtas - 1, ROWS < most_rows ? ROWS : most_rows),
+                    dim3(kAqJoinWarps * 32), 0, st, a);
 }
 
 }  // namespace
@@ -723,7 +773,7 @@ namespace {
 size_t stream_workspace_bytes(const Shape& sh, int n_tokens, int max_q) {
   if (small_rows(sh, max_q) == 0) return 0;
   const size_t slots = (size_t)kAqMaxCtas + (size_t)max_items(sh, n_tokens, max_q);
-  const size_t bytes = slots * item_rows(sh, max_q) * (sh.D + 2) * sizeof(float);
+  const size_t bytes = slots * item_rows(sh, max_q) * (sh.D + 2) * sizeof(float) + kAqMaxCtas * sizeof(JoinJob);
   return (bytes + 255) / 256 * 256;
 }
 }  // namespace
@@ -745,12 +795,12 @@ bool attn_q8_fits(const Shape& sh, int max_q, int max_seq_len) {
 int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, const AttnQ8Call& c, void* ws,
                    cudaStream_t st) {
   AttnQ8Args a;
-  const unsigned long long rows = ((unsigned long long)pool.n_blocks * sh.Hkv) << pool.log_bs;
+  const unsigned long long pool_rows = ((unsigned long long)pool.n_blocks * sh.Hkv) << pool.log_bs;
   const unsigned box = pool.log_bs == 4 ? 16 : kAqTile;
   const CUtensorMapSwizzle sw = sh.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (!make_tensor_map(&a.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool.k, sh.D, rows, sh.D, box, sw,
+  if (!make_tensor_map(&a.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool.k, sh.D, pool_rows, sh.D, box, sw,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-      !make_tensor_map(&a.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool.v, sh.D, rows, sh.D, box, sw,
+      !make_tensor_map(&a.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool.v, sh.D, pool_rows, sh.D, box, sw,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B)) {
     set_error("attn q8: could not encode the K/V tensor maps (cuTensorMapEncodeTiled)");
     return RTP_ERR_CUDA;
@@ -768,8 +818,9 @@ int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, co
   for (int i = 0; i < 64; ++i) a.turns[i] = sh.turns[i];
   a.small_rows = small_rows(sh, c.max_q);
   const long long items = max_items(sh, c.n_tokens, c.max_q);
-  a.part = static_cast<float*>(ws);
-  a.n_slots = kAqMaxCtas + items;
+  a.jobs = static_cast<JoinJob*>(ws);
+  a.part = reinterpret_cast<float*>(a.jobs + kAqMaxCtas);
+  a.n_slots = (uint32_t)(kAqMaxCtas + items);
   a.part_ml = a.part + (size_t)a.n_slots * a.rows * sh.D;
   const bool chunks = a.small_rows != INT32_MAX;
   if (chunks && !chunk_carve(sh, c.n_tokens, c.max_q, a.small_rows,
@@ -780,11 +831,13 @@ int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, co
   cudaError_t e = cudaSuccess;
   trace_begin(RTP_STAGE_ATTN_Q8, st);
   if (a.small_rows > 0) {
+    const long long rows = (long long)small_q(sh, c.max_q) * sh.G;  // that a request can have
+    const int most = rows < 16 ? (int)rows : 16;
     if (sh.dtype == RTP_BF16) {
-      if (a.rows == 8) e = sh.D == 128 ? launch<__nv_bfloat16, 128, 8>(a, st) : launch<__nv_bfloat16, 64, 8>(a, st);
-      else e = sh.D == 128 ? launch<__nv_bfloat16, 128, 16>(a, st) : launch<__nv_bfloat16, 64, 16>(a, st);
+      if (a.rows == 8) e = sh.D == 128 ? launch<__nv_bfloat16, 128, 8>(a, most, st) : launch<__nv_bfloat16, 64, 8>(a, most, st);
+      else e = sh.D == 128 ? launch<__nv_bfloat16, 128, 16>(a, most, st) : launch<__nv_bfloat16, 64, 16>(a, most, st);
     } else {
-      e = sh.D == 128 ? launch<float, 128, 8>(a, st) : launch<float, 64, 8>(a, st);
+      e = sh.D == 128 ? launch<float, 128, 8>(a, most, st) : launch<float, 64, 8>(a, most, st);
     }
   }
   if (chunks && e == cudaSuccess) e = launch_attn_q8_chunks(sh, a, st);

@@ -20,20 +20,27 @@ struct __align__(16) ChunkItem {
   int ns, w0, ret, pad;
 };
 
+// An item that the cut behind a CTA's share goes through first: its partials
+// lie in slots [slot0, slot0 + np); np = 0: there is none.
+struct __align__(16) JoinJob {
+  int np, n_rows;
+  uint32_t slot0;
+  int h, row0, q0, pad0, pad1;
+};
+
 struct __align__(64) AttnQ8Args {
-  CUtensorMap tm_k, tm_v;  // the pool as [n_blocks Hkv block_size][D] bytes, boxes of min(32, block_size) rows
+  // first what every CTA reads at once (each line of the parameters misses at a kernel's start)
+  AttnQ8Call c;
   Q8Pool pool;
-  RopeAxes rope;
   int B, Hq, Hkv, G, S, W, rows;
   int log_g;          // G is a power of two
   int small_rows;     // requests of more query rows (n G) a KV head go to the chunk kernel
-  long long n_slots;  // partials that the workspace holds
+  uint32_t n_slots;   // partials that the workspace holds
   uint64_t ret_mask;
-  AttnQ8Call c;
-  float* part;  // [n_cta + items][rows][D] O, then [..][rows][2] (M, l)
+  float* part;        // [n_slots][rows][D] O, and (M, l)
   float* part_ml;
+  JoinJob* jobs;  // [CTAs] what each cut of the line leaves to join
   unsigned long long wait_ns;
-  uint64_t turns[64];  // rotary frequencies
   // the chunk kernel's share of the workspace
   ChunkItem* items;
   long long* prefix;  // tiles ahead of each item, then their number; [max_chunk_items + 1]: a CTA's share of them
@@ -43,10 +50,12 @@ struct __align__(64) AttnQ8Args {
   int max_chunk_items;
   __half* cq;         // rotated queries, [n_tokens][Hq][D], each row by its power-of-two scale
   float* cq_unit;     // [n_tokens][Hq]: from their products to base-2 logits
-  CUtensorMap tm_q;   // cq, boxes of 64 dims x G heads x 128 / G tokens
-  CUtensorMap tm_ck, tm_cv;  // the pool as rows of D bytes, boxes of min(64, block_size) rows
+  uint64_t turns[64]; // rotary frequencies
+  RopeAxes rope;
+  CUtensorMap tm_k, tm_v;    // the pool as [n_blocks Hkv block_size][D] bytes, boxes of min(32, block_size) rows
+  CUtensorMap tm_q;          // cq, boxes of 64 dims x G heads x 128 / G tokens
+  CUtensorMap tm_ck, tm_cv;  // the pool as rows of D bytes, boxes of min(128, block_size) rows
 };
-
 
 // First packed row, number of queries and cached positions of request b;
 // n = 0 where it has nothing to do or is refused (`flags`).

@@ -35,6 +35,20 @@ __device__ __forceinline__ float q8_scale(float a) {
 // 1 / s of a power of two 2^-64 <= s <= 2^121, exactly.
 __device__ __forceinline__ float q8_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+// An element of a table among a kernel's parameters, by an ordinary load: lanes
+// that index the constant bank apart are served one after another, and each of
+// its lines misses at a kernel's start.
+__device__ __forceinline__ uint64_t table_at(const uint64_t* t, int k) {
+  uint64_t x;
+  asm volatile("ld.u64 %0, [%1];" : "=l"(x) : "l"(t + k));
+  return x;
+}
+__device__ __forceinline__ int table_at(const unsigned char* t, int k) {
+  uint32_t x;
+  asm volatile("ld.u8 %0, [%1];" : "=r"(x) : "l"(t + k));
+  return (int)x;
+}
+
 // cos and sin of a rotary angle from its frequency in turns (0.64 fixed
 // point): the product with the position wraps around modulo one turn, so no
 // position is too far for the reduction, and what is left goes to fp32 once.
