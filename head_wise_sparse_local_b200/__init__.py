@@ -197,66 +197,83 @@ def rtp_q8_cache_bytes(cfg: rtp_layer_cfg, n_blocks: int, block_size: int):
     return kv.value, sc.value
 
 
-def _here(x, name) -> None:
-    """Kernels run on the current device: a tensor of another one is refused."""
-    if x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+def _arg(x, dtype, name, dev, n=-1) -> int:
+    """Address of a dense tensor whose element type, device and number of elements the call fixes.
+    Kernels run on the current device `dev`: a tensor of another one is refused."""
+    if x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous() or (n >= 0 and x.numel() != n):
+        _refuse(x, dtype, name, dev, n)
+    return x.data_ptr()
 
 
-def _arg(x, dtype, name) -> Optional[int]:
-    """_ptr of a tensor whose element type the library fixes."""
-    if x.dtype != dtype:
+def _refuse(x, dtype, name, dev, n) -> None:
+    if x.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}")
-    p = _ptr(x)
-    _here(x, name)
-    return p
+    if not x.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    raise ValueError(f"{name} must have {n} elements")
 
 
-def _packed(x, cfg, heads: int, name):
+def _packed(x, cfg, heads: int, name, dev):
     """(address, elements between tokens) of packed [N, heads, D] rows, dense or a slice of wider rows."""
+    D = cfg.head_dim
     dt = torch.bfloat16 if cfg.dtype == RTP_BF16 else torch.float32
-    if not x.is_cuda or x.dtype != dt or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != cfg.head_dim:
-        raise ValueError(f"{name} must be a CUDA [N, {heads}, {cfg.head_dim}] tensor of {dt}")
-    _here(x, name)
-    s = x.stride()
-    if (s[2] != 1 or s[1] != cfg.head_dim) and x.numel() > 0:
+    shape = x.shape
+    if x.dtype is not dt or len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} must be a CUDA [N, {heads}, {D}] tensor of {dt}")
+    if x.get_device() != dev:
+        _refuse(x, dt, name, dev, -1)
+    s0, s1, s2 = x.stride()
+    if (s2 != 1 or s1 != D) and shape[0] > 0:
         raise ValueError(f"{name}: a token's heads must be dense")
-    return x.data_ptr(), s[0] if x.shape[0] > 1 else 0
+    return x.data_ptr(), s0 if shape[0] > 1 else 0
 
 
-def _axes(pos, rope, n) -> int:
-    if pos.dtype != torch.int32 or pos.numel() != n * (rope.n_axes if rope is not None else 1):
-        raise ValueError("pos must be int32 [n_axes, N]")
-    return _arg(pos, torch.int32, "pos")
+def _device(x, name) -> int:
+    """The device of a call's first tensor, which has to be the current one."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {x.device}, not on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def rtp_page_plan(cfg, block_size, ctx_len, new_len, block_table, free_list, n_free, seq_len, cu_new,
                   slot_map, positions, n_free_out, status, stream=None) -> None:
-    i32 = torch.int32
+    i32, dev, B = torch.int32, _device(ctx_len, "ctx_len"), cfg.batch
     cols = -(-cfg.max_ctx // block_size) if block_size > 0 else 0
-    for name, x, n in (("ctx_len", ctx_len, cfg.batch), ("new_len", new_len, cfg.batch), ("seq_len", seq_len, cfg.batch),
-                       ("cu_new", cu_new, cfg.batch + 1), ("block_table", block_table, cfg.batch * cols),
-                       ("positions", positions, slot_map.numel())):
-        if x.numel() != n:
-            raise ValueError(f"{name} must have {n} elements")
-    _abi.check(_lib.rtp_page_plan(ctypes.byref(cfg), int(block_size), _arg(ctx_len, i32, "ctx_len"),
-                                  _arg(new_len, i32, "new_len"), _arg(block_table, i32, "block_table"),
-                                  _arg(free_list, i32, "free_list"), free_list.numel(), _arg(n_free, i32, "n_free"),
-                                  _arg(seq_len, i32, "seq_len"), _arg(cu_new, i32, "cu_new"),
-                                  _arg(slot_map, torch.int64, "slot_map"), _arg(positions, i32, "positions"),
-                                  slot_map.numel(), _arg(n_free_out, i32, "n_free_out"), _arg(status, i32, "status"),
-                                  _stream(stream)))
+    n = slot_map.numel()
+    rc = _lib.rtp_page_plan(cfg, block_size, _arg(ctx_len, i32, "ctx_len", dev, B), _arg(new_len, i32, "new_len", dev, B),
+                            _arg(block_table, i32, "block_table", dev, B * cols), _arg(free_list, i32, "free_list", dev),
+                            free_list.numel(), _arg(n_free, i32, "n_free", dev, 1), _arg(seq_len, i32, "seq_len", dev, B),
+                            _arg(cu_new, i32, "cu_new", dev, B + 1), _arg(slot_map, torch.int64, "slot_map", dev),
+                            _arg(positions, i32, "positions", dev, n), n, _arg(n_free_out, i32, "n_free_out", dev, 1),
+                            _arg(status, i32, "status", dev, 1), _raw_stream(stream, dev))
+    if rc:
+        _abi.check(rc)
 
 
 def rtp_append_q8(cfg, cache, k_pre, v_in, slot_map, pos, rope=None, stream=None) -> None:
-    n = k_pre.shape[0]
-    k, ks = _packed(k_pre, cfg, cfg.n_kv_heads, "k_pre")
-    v, vs = _packed(v_in, cfg, cfg.n_kv_heads, "v_in")
-    if v_in.shape[0] != n or slot_map.numel() != n:
-        raise ValueError("k_pre, v_in and slot_map must have as many tokens")
-    _abi.check(_lib.rtp_append_q8(ctypes.byref(cfg), ctypes.byref(cache), k, ks, v, vs,
-                                  _arg(slot_map, torch.int64, "slot_map"), _axes(pos, rope, n),
-                                  None if rope is None else ctypes.byref(rope), n, _stream(stream)))
+    dev, n = _device(k_pre, "k_pre"), k_pre.shape[0]
+    k, ks = _packed(k_pre, cfg, cfg.n_kv_heads, "k_pre", dev)
+    v, vs = _packed(v_in, cfg, cfg.n_kv_heads, "v_in", dev)
+    if v_in.shape[0] != n:
+        raise ValueError("k_pre and v_in must have as many tokens")
+    rc = _lib.rtp_append_q8(cfg, cache, k, ks, v, vs, _arg(slot_map, torch.int64, "slot_map", dev, n),
+                            _arg(pos, torch.int32, "pos", dev, n * (rope.n_axes if rope is not None else 1)), rope, n,
+                            _raw_stream(stream, dev))
+    if rc:
+        _abi.check(rc)
 
 
 def rtp_attn_q8_workspace_bytes(cfg: rtp_layer_cfg, block_size: int, n_tokens: int, max_q: int,
@@ -269,21 +286,21 @@ def rtp_attn_q8_workspace_bytes(cfg: rtp_layer_cfg, block_size: int, n_tokens: i
 
 def rtp_attn_q8(cfg, cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, max_seq_len=0, rope=None,
                 workspace=None, workspace_bytes=0, stream=None) -> None:
-    n = q_pre.shape[0]
-    q, qs = _packed(q_pre, cfg, cfg.n_q_heads, "q_pre")
-    i32 = torch.int32
     if workspace is None:
         raise ValueError("workspace is missing: rtp_attn_q8_workspace_bytes says how much")
+    i32, dev, n, B = torch.int32, _device(q_pre, "q_pre"), q_pre.shape[0], cfg.batch
+    q, qs = _packed(q_pre, cfg, cfg.n_q_heads, "q_pre", dev)
     if out.shape != q_pre.shape:
         raise ValueError("out must have q_pre's shape")
-    if cu_q.numel() != cfg.batch + 1 or seq_len.numel() != cfg.batch or \
-            block_table.numel() != cfg.batch * -(-cfg.max_ctx // cache.block_size):
-        raise ValueError("cu_q, seq_len or block_table does not fit the batch")
-    _abi.check(_lib.rtp_attn_q8(ctypes.byref(cfg), ctypes.byref(cache), q, qs, _arg(cu_q, i32, "cu_q"),
-                                _arg(seq_len, i32, "seq_len"), _arg(block_table, i32, "block_table"),
-                                _axes(pos, rope, n), None if rope is None else ctypes.byref(rope), n, int(max_q),
-                                int(max_seq_len), _arg(out, q_pre.dtype, "out"), _arg(workspace, torch.uint8, "workspace"),
-                                int(workspace_bytes), _stream(stream)))
+    if workspace.numel() < workspace_bytes:
+        raise ValueError("workspace_bytes is more than the workspace has")
+    rc = _lib.rtp_attn_q8(cfg, cache, q, qs, _arg(cu_q, i32, "cu_q", dev, B + 1), _arg(seq_len, i32, "seq_len", dev, B),
+                          _arg(block_table, i32, "block_table", dev, B * -(-cfg.max_ctx // cache.block_size)),
+                          _arg(pos, i32, "pos", dev, n * (rope.n_axes if rope is not None else 1)), rope, n, max_q,
+                          max_seq_len, _arg(out, q_pre.dtype, "out", dev), _arg(workspace, torch.uint8, "workspace", dev),
+                          workspace_bytes, _raw_stream(stream, dev))
+    if rc:
+        _abi.check(rc)
 
 
 class PagedLayer:
