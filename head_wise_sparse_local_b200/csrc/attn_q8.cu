@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     };
     auto load_pair = [&](int task, Pair& y) {
       const int tl = task / (D / 2), k = task % (D / 2), tok = rq.q0 + tok0 + tl;
-      y.turns = table_at(a.turns, k);
-      y.pos = a.c.pos[(size_t)(a.rope.n_axes > 1 ? table_at(a.rope.axis, k) : 0) * a.c.n_tokens + tok];
+      y.turns = a.turns[k];
+      y.pos = a.c.pos[(size_t)(a.rope.n_axes > 1 ? a.rope.axis[k] : 0) * a.c.n_tokens + tok];
       y.ra = max(((tok0 + tl) << a.log_g) - row0, 0);
       y.rb = min(((tok0 + tl + 1) << a.log_g) - row0, n_rows);
       const T* q = static_cast<const T*>(a.c.q_pre) + (size_t)tok * a.c.q_stride +

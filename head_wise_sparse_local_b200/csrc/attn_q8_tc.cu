@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < PP; ++i) {
       const int k = lane * PP + i;
-      rope_turns(a.c.pos[(size_t)table_at(a.rope.axis, k) * a.c.n_tokens + t], table_at(a.turns, k), c[i], s[i]);
+      rope_turns(a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + t], a.turns[k], c[i], s[i]);
     }
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.c.q_pre) + (size_t)t * a.c.q_stride + (size_t)h0 * D + lane * PP;
     const int nh = min(a.Hq - h0, 8);

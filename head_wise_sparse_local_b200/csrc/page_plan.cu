@@ -3,7 +3,7 @@
 //
 // Everything follows from three prefix sums over the requests (blocks that
 // ended requests give back, blocks that the others need, tokens that they
-// bring), so one launch does it all: a cluster of 1 to 8 CTAs, each of which
+// bring), so one launch does it all: a cluster of 1 to 16 CTAs, each of which
 // forms the sums for itself (B lengths, a few KB from L2) and then writes its
 // share of the tables and of the token arrays.  The one cluster barrier stands
 // between "every CTA has read the lengths and the stack's height, and the
@@ -20,7 +20,7 @@ namespace rtp {
 namespace {
 
 constexpr int kPlanMaxThreads = 1024;
-constexpr int kPlanMaxCluster = 8;  // the largest portable cluster
+constexpr int kPlanMaxCluster = 16;  // the largest cluster (more than 8 have to be asked for)
 
 struct PlanArgs {
   int B, log_bs, cols, free_cap, max_tokens, max_ctx;
@@ -47,6 +47,19 @@ struct PlanReq {
 
 __device__ __forceinline__ void cluster_arrive_wait() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// to[i] = from[dir i] for i = first, first + step, .. below n, eight loads on their way at once.
+__device__ __forceinline__ void copy_ids(int* to, const int* from, int dir, int first, int n, int step) {
+  for (int i0 = first; i0 < n; i0 += 8 * step) {
+    int v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * step < n) v[k] = from[dir * (i0 + k * step)];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * step < n) to[i0 + k * step] = v[k];
+  }
 }
 
 __global__ void __launch_bounds__(kPlanMaxThreads) page_plan_kernel(const __grid_constant__ PlanArgs a) {
@@ -99,15 +112,18 @@ __global__ void __launch_bounds__(kPlanMaxThreads) page_plan_kernel(const __grid
     if (lane == 31)
       for (int k = 0; k < 3; ++k) s_warp[k][warp] = x[k];
     __syncthreads();
-    long long tot[3] = {0, 0, 0};
+    long long tot[3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      long long before = 0;
-      for (int w = 0; w < nwarp; ++w) {
-        if (w < warp) before += s_warp[k][w];
-        tot[k] += s_warp[k][w];
+    for (int k = 0; k < 3; ++k) {  // the warps' sums, a lane each
+      long long y = lane < nwarp ? s_warp[k][lane] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
       }
-      x[k] += run[k] + before - v[k];  // exclusive
+      tot[k] = __shfl_sync(0xffffffffu, y, 31);
+      const long long before = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
+      x[k] += run[k] + (warp > 0 ? before : 0) - v[k];  // exclusive
     }
     if (b < a.B) {
       // sums past the stack or the token arrays only have to stay past them
@@ -123,14 +139,17 @@ __global__ void __launch_bounds__(kPlanMaxThreads) page_plan_kernel(const __grid
   const int top = (int)min(height + run[0], (long long)a.free_cap);
   if (tid == 0) s_req[a.B].cu = n_tok;
   __syncthreads();
-  // ---- ended requests' blocks onto the stack ----
-  if (run[0] > 0) {
-    for (int b = rank * nwarp + warp; b < a.B; b += n_cta * nwarp) {
+  // ---- ended requests' blocks onto the stack (`per` warps a request) ----
+  const int all_warps = n_cta * nwarp, per = max(1, all_warps / a.B);
+  const int my_req = (rank * nwarp + warp) / per, my_first = (rank * nwarp + warp) % per * 32 + lane;
+  if (run[0] > 0 && my_req * per + per <= all_warps) {
+    for (int b = my_req; b < a.B; b += all_warps / per) {
       const PlanReq r = s_req[b];
       if (r.add >= 0) continue;
-      const int have = (r.ctx + bs1) >> a.log_bs;
-      for (int i = lane; i < have; i += 32)
-        if (r.base + (long long)i < a.free_cap) a.free_list[r.base + i] = a.table[(size_t)b * a.cols + i];
+      const int have = (int)min((long long)((r.ctx + bs1) >> a.log_bs), (long long)a.free_cap - r.base);
+      const int* from = a.table + (size_t)b * a.cols;
+      int* to = a.free_list + r.base;
+      copy_ids(to, from, 1, my_first, have, per * 32);
     }
   }
   cluster_arrive_wait();
@@ -164,12 +183,16 @@ __global__ void __launch_bounds__(kPlanMaxThreads) page_plan_kernel(const __grid
     *a.n_free_out = top - s_taken;
   }
   // ---- table entries of the blocks taken ----
-  for (int b = rank * nwarp + warp; b < a.B; b += n_cta * nwarp) {
-    const PlanReq r = s_req[b];
-    if (r.add <= 0) continue;
-    const int have = (r.ctx + bs1) >> a.log_bs;
-    const int need = ((r.ctx + r.add + bs1) >> a.log_bs) - have;
-    for (int i = lane; i < need; i += 32) a.table[(size_t)b * a.cols + have + i] = a.free_list[r.base - i];
+  if (my_req * per + per <= all_warps) {
+    for (int b = my_req; b < a.B; b += all_warps / per) {
+      const PlanReq r = s_req[b];
+      if (r.add <= 0) continue;
+      const int have = (r.ctx + bs1) >> a.log_bs;
+      const int need = ((r.ctx + r.add + bs1) >> a.log_bs) - have;
+      const int* from = a.free_list + r.base;
+      int* to = a.table + (size_t)b * a.cols + have;
+      copy_ids(to, from, -1, my_first, need, per * 32);
+    }
   }
   // ---- slots and positions, four consecutive tokens a thread ----
   for (int t0 = (rank * nthr + tid) * 4; t0 < a.max_tokens; t0 += n_cta * nthr * 4) {
@@ -185,21 +208,31 @@ __global__ void __launch_bounds__(kPlanMaxThreads) page_plan_kernel(const __grid
       }
       next = s_req[b + 1].cu;
     }
+    PlanReq r = s_req[b];
+    int have = (r.ctx + bs1) >> a.log_bs;
+    int col = -1, blk = -1;  // the block of the last token looked up (four tokens are seldom in more than one)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int t = t0 + e;
       slot[e] = -1;
       pos[e] = 0;
       if (t >= n_tok) continue;
-      while (t >= next) next = s_req[++b + 1].cu;  // t < n_tok = cu of the end
-      const PlanReq r = s_req[b];
+      if (t >= next) {
+        while (t >= next) next = s_req[++b + 1].cu;  // t < n_tok = cu of the end
+        r = s_req[b];
+        have = (r.ctx + bs1) >> a.log_bs;
+        col = -1;
+      }
       const int p = r.ctx + t - r.cu;
       pos[e] = p;
       if (r.add < 0) continue;
-      const int c = p >> a.log_bs, have = (r.ctx + bs1) >> a.log_bs;
-      const int blk = c < have ? a.table[(size_t)b * a.cols + c] : a.free_list[r.base - (c - have)];
+      const int c = p >> a.log_bs;
+      if (c != col) {
+        col = c;
+        blk = c < have ? a.table[(size_t)b * a.cols + c] : a.free_list[r.base - (c - have)];
+        if (blk < 0) flags |= RTP_DEV_BLOCKS;
+      }
       if (blk >= 0) slot[e] = ((int64_t)blk << a.log_bs) + (p & bs1);
-      else flags |= RTP_DEV_BLOCKS;
     }
     if (t0 + 4 <= a.max_tokens) {
       reinterpret_cast<longlong2*>(a.slot_map + t0)[0] = make_longlong2(slot[0], slot[1]);
@@ -247,7 +280,8 @@ int launch_page_plan(const Shape& sh, int log_bs, int table_cols, const int* ctx
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cudaError_t e = cudaSuccess;
-  if (cfg.dynamicSmemBytes > 40 * 1024)  // past what a kernel may take unasked
+  if (n_cta > 8) e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && cfg.dynamicSmemBytes > 40 * 1024)  // past what a kernel may take unasked
     e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)((kMaxPlanBatch + 1) * sizeof(PlanReq)));
   trace_begin(RTP_STAGE_PAGE_PLAN, st);

@@ -35,26 +35,29 @@ __device__ __forceinline__ float q8_scale(float a) {
 // 1 / s of a power of two 2^-64 <= s <= 2^121, exactly.
 __device__ __forceinline__ float q8_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
-// An element of a table among a kernel's parameters, by an ordinary load: lanes
-// that index the constant bank apart are served one after another, and each of
-// its lines misses at a kernel's start.
-__device__ __forceinline__ uint64_t table_at(const uint64_t* t, int k) {
-  uint64_t x;
-  asm volatile("ld.u64 %0, [%1];" : "=l"(x) : "l"(t + k));
-  return x;
-}
-__device__ __forceinline__ int table_at(const unsigned char* t, int k) {
-  uint32_t x;
-  asm volatile("ld.u8 %0, [%1];" : "=r"(x) : "l"(t + k));
-  return (int)x;
-}
-
 // cos and sin of a rotary angle from its frequency in turns (0.64 fixed
-// point): the product with the position wraps around modulo one turn, so no
-// position is too far for the reduction, and what is left goes to fp32 once.
+// point).  The product with the position wraps around modulo one turn, so no
+// position is too far for the reduction; its upper 32 bits split into the
+// nearest quarter turn and a rest within an eighth, whose sine and cosine are
+// Taylor sums (to r^9 and r^10: off by less than 2^-26).  Off by 2^-23 at most.
 __device__ __forceinline__ void rope_turns(int pos, uint64_t turns, float& c, float& s) {
-  const long long frac = (long long)((uint64_t)(long long)pos * turns);  // [-1/2, 1/2) turn, times 2^64
-  sincospif(__ll2float_rn(frac) * 1.0842021724855044e-19f, &s, &c);     // half turns: 2^-63
+  const uint32_t lo = (uint32_t)turns, p = (uint32_t)pos;
+  const uint32_t f = __umulhi(p, lo) + p * (uint32_t)(turns >> 32) - (pos < 0 ? lo : 0u);
+  const uint32_t q = (f + 0x20000000u) >> 30;                                  // quarter turns
+  const float r = (float)(int)(f - (q << 30)) * 1.4629180792671596e-09f;      // the rest, 2 pi / 2^32
+  const float x = r * r;
+  float sn = fmaf(x, 2.7557319e-06f, -1.9841270e-04f);
+  sn = fmaf(sn, x, 8.3333333e-03f);
+  sn = fmaf(sn, x, -1.6666667e-01f);
+  sn = fmaf(sn * x, r, r);
+  float cs = fmaf(x, -2.7557319e-07f, 2.4801587e-05f);
+  cs = fmaf(cs, x, -1.3888889e-03f);
+  cs = fmaf(cs, x, 4.1666667e-02f);
+  cs = fmaf(cs, x, -0.5f);
+  cs = fmaf(cs, x, 1.f);
+  const float u = q & 1u ? sn : cs, v = q & 1u ? cs : sn;
+  c = __uint_as_float(__float_as_uint(u) ^ (((q + 1u) & 2u) << 30));  // cos: minus in quarters 1 and 2
+  s = __uint_as_float(__float_as_uint(v) ^ ((q & 2u) << 30));       // sin: minus in quarters 2 and 3
 }
 
 }  // namespace rtp
