@@ -74,7 +74,7 @@ struct CSmem {
 
 // Scales of 16 positions of a tile, and which 32-position words are there.
 struct __align__(16) CMeta {
-  float4 g[8];  // k scale, log2(v scale), 1 / v scale
+  float4 g[8];  // k scale, log2(v scale), 1 / v scale; g[0].w: 1 where all are there
   uint32_t there[4];
 };
 
@@ -375,7 +375,7 @@ __device__ __forceinline__ bool load_rows_of_tile(const AttnQ8Args& a, const CWa
   CMeta& m = meta[T & 7];
   const unsigned there = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
   vs = fmaxf(vs, kQ8ScaleMin);
-  if (lane < 8) m.g[lane] = make_float4(fmaxf(ks, kQ8ScaleMin), __log2f(vs), 1.f / vs, 0.f);
+  if (lane < 8) m.g[lane] = make_float4(fmaxf(ks, kQ8ScaleMin), __log2f(vs), 1.f / vs, there == 0xffu ? 1.f : 0.f);
   if (lane < 4)
     m.there[lane] = ((there >> (2 * lane) & 1u) ? 0xffffu : 0u) | ((there >> (2 * lane + 1) & 1u) ? 0xffff0000u : 0u);
   __syncwarp();
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
         tc_fence_after();
         const CMeta& m = s_meta[(gt + i) & 7];
         const bool whole = kt + kCKeys - 1 <= s_lo && (c.ret || kt + kCKeys - 1 < a.S || kt > s_hi - a.W) &&
-                           (m.there[0] & m.there[1] & m.there[2] & m.there[3]) == 0xffffffffu;
+                           m.g[0].w != 0.f;
         if (!whole) {  // (the slot agrees) S of the positions that the row does not see becomes -inf
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {
@@ -484,39 +484,19 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
           }
           tmem_wait_st();
         }
-        // ---- the weights against the running maximum, 32 columns at a time while the next
-        // are on their way, their fp16 over columns already read ----
-        auto weigh = [&](const float (&v)[32], int x) {
-          uint32_t pk[16];
-          float mx, sum;
-          auto form = [&]() {
-            const float base = kAqLift - (M == -CUDART_INF_F ? 0.f : M);
-            sum = 0.f;
+        // ---- the weights against the running maximum, 64 columns at a time (one rolled loop:
+        // the instruction cache feeds it), their fp16 over columns already read ----
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          float v[64];
+          tmem_ld64(tSs + 64 * x, v);
+          float4 g[4];  // of 16 columns each
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float4 g = m.g[2 * x + q];
-              const float fq = rs * g.x, add = g.y + base;
-              float s0 = 0.f, s1 = 0.f;
+          for (int q = 0; q < 4; ++q) g[q] = m.g[4 * x + q];
+          tmem_wait_ld();
+          float mx = -CUDART_INF_F;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float x0 = v[16 * q + 2 * e], x1 = v[16 * q + 2 * e + 1];
-                fma2(x0, x1, fq, add);
-                if ((e & 3) == 3) {  // one weight in four on the FMA pipe
-                  ex2_poly2(x0, x1);
-                } else {
-                  x0 = ex2f(x0);
-                  x1 = ex2f(x1);
-                }
-                add2(s0, s1, x0, x1);
-                pk[8 * q + e] = pack_f16(x0, x1);
-              }
-              sum = fmaf(s0 + s1, g.z, sum);
-            }
-          };
-          form();
-          mx = -CUDART_INF_F;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             const float* y = v + 16 * q;
             float t0 = max3_nan(y[0], y[1], y[2]), t1 = max3_nan(y[3], y[4], y[5]);
             t0 = max3_nan(t0, y[6], y[7]);
@@ -524,8 +504,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
             t0 = max3_nan(t0, y[10], y[11]);
             t1 = max3_nan(t1, y[12], y[13]);
             t0 = max3_nan(t0, y[14], y[15]);
-            const float4 g = m.g[2 * x + q];
-            mx = max_nan(mx, fmaf(max_nan(t0, t1), rs * g.x, g.y));
+            mx = max_nan(mx, fmaf(max_nan(t0, t1), rs * g[q].x, g[q].y));
           }
           poison = poison || mx != mx;  // a stored NaN that the row sees
           const bool need = mx > M + kCRescale || (M == -CUDART_INF_F && mx > M);
@@ -550,7 +529,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
             tmem_wait_st();
             const __half2 f2 = __float2half2_rn(f);
 #pragma unroll 1
-            for (int y = 0; y < x; ++y) {
+            for (int y = 0; y < 2 * x; ++y) {
               uint32_t o[16];
               tmem_ld16(tSs + y * 16, o);
               tmem_wait_ld();
@@ -561,22 +540,31 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
               }
               tmem_st16(tSs + y * 16, o);
             }
-            form();
           }
-          l += sum;
-          tmem_st16(tSs + 16 * x, pk);
-        };
-        {
-          float v0[32], v1[32];
-          tmem_ld32(tSs, v0);
-#pragma unroll 1
-          for (int x = 0; x < 4; x += 2) {
-            tmem_wait_ld();
-            tmem_ld32(tSs + 32 * x + 32, v1);
-            weigh(v0, x);
-            tmem_wait_ld();
-            if (x == 0) tmem_ld32(tSs + 64, v0);
-            weigh(v1, x + 1);
+          const float base = kAqLift - (M == -CUDART_INF_F ? 0.f : M);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float fq = rs * g[2 * w + q].x, add = g[2 * w + q].y + base;
+              float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float x0 = v[32 * w + 16 * q + 2 * e], x1 = v[32 * w + 16 * q + 2 * e + 1];
+                fma2(x0, x1, fq, add);
+                if ((e & 3) == 3) {  // one weight in four on the FMA pipe
+                  ex2_poly2(x0, x1);
+                } else {
+                  x0 = ex2f(x0);
+                  x1 = ex2f(x1);
+                }
+                add2(s0, s1, x0, x1);
+                pk[8 * q + e] = pack_f16(x0, x1);
+              }
+              l = fmaf(s0 + s1, g[2 * w + q].z, l);
+            }
+            tmem_st16(tSs + 32 * x + 16 * w, pk);
           }
         }
         tmem_wait_st();
@@ -654,7 +642,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
         const CMeta& m = s_meta[T & 7];
         const int n_valid = w.c.i_hi - tile_pos(w.c, w.u0 + i) + 1;
         if (!(ok = c_wait(&bars.raw_full[0], (uint32_t)T & 1u, a, &s_abort))) break;
-        const bool all = n_valid >= kCKeys && (m.there[0] & m.there[1] & m.there[2] & m.there[3]) == 0xffffffffu;
+        const bool all = n_valid >= kCKeys && m.g[0].w != 0.f;
         if (!(ok = c_wait(&bars.k_empty[st], par, a, &s_abort))) break;
         convert(dsm + SM::kOffRaw, dsm + SM::kOffK + st * SM::kOp, m, n_valid, all);
         fence_async_smem();
