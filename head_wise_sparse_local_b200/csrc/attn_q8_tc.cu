@@ -57,7 +57,8 @@ constexpr int kCKeys = 128;               // positions a tile
 constexpr int kCThreads = 16 * 32;
 constexpr int kCRegion = 128 * 128;       // bytes of 128 rows x 64 fp16 dims
 constexpr int kCCtas = 148;               // one an SM of a B200
-constexpr int kCMinShare = 4;             // tiles a CTA takes at least: a segment's start and end cost about as much
+constexpr int kCItemCost = 3;             // units of the line after an item's tiles: its start and end cost about as much
+constexpr int kCMinShare = 4;             // units a CTA takes at least
 constexpr int kCTmemCols = 512;
 constexpr float kCRescale = 9.f;          // the running maximum moves past 2^9: weights reach 2^15, below fp16's largest
 
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
       const ReqRows r = load_rows(a, b, flags);
       const int ng = (r.n * a.G + kCGroup - 1) / kCGroup, rel = i - a.req_items[b];
       it = chunk_item(a, r, b, rel / ng, rel % ng);
-      v = it.tiles;
+      v = it.tiles + kCItemCost;
     }
     long long total;
     const long long x = tiles + block_scan(v, total, s_warp);
@@ -333,17 +334,16 @@ struct CWalk {
     if (at >= end) return false;
     item = find_item(a.prefix, n_items, at);
     load(a);
-    return true;
+    return nt > 0 || next(a);
   }
   __device__ __forceinline__ void load(const AttnQ8Args& a) {
     c = a.items[item];
     u0 = (int)(at - a.prefix[item]);
-    nt = (int)min((long long)c.tiles - u0, end - at);
+    nt = (int)min((long long)c.tiles - u0, end - at);  // none or fewer if the share starts in the units after the item's tiles
     two = c.n_rows > kCRows;
   }
   __device__ __forceinline__ bool next(const AttnQ8Args& a) {
-    at += nt;
-    ++item;
+    at = a.prefix[++item];
     if (at >= end) return false;
     load(a);
     return true;
@@ -815,8 +815,9 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
   const int item = find_item(a.prefix, n_items, at);
   const long long first = a.prefix[item];
   if (first == at || at - share > first) return;  // between two items, or not the item's first cut
-  const int c1 = (int)((a.prefix[item + 1] - 1) / share);
   const ChunkItem c = a.items[item];
+  if (at - first >= c.tiles) return;
+  const int c1 = (int)((first + c.tiles - 1) / share);
   const int r = blockIdx.y * (256 / LPR) + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
   if (r >= c.n_rows) return;
   // the share that starts the item keeps its partial second, the later ones first
