@@ -306,7 +306,10 @@ def rtp_attn_q8(cfg, cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, 
 class PagedLayer:
     """One layer's configuration with a pool of 8-bit blocks and scratch, all
     torch-allocated.  Requests' block tables come from rtp_page_plan and are
-    shared by a model's layers; pass the step's to append() and attend()."""
+    shared by a model's layers; pass the step's to append() and attend().
+    attend() calls share one scratch, so they must not overlap each other;
+    layers that run side by side, and graphs replayed side by side, take an
+    object each."""
 
     def __init__(self, shape, max_ctx: int, n_blocks: int, block_size: int = 64, device="cuda", rope=None):
         self.shape = shape
@@ -322,12 +325,16 @@ class PagedLayer:
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.cache = make_q8_cache(self.k, self.v, self.k_scale, self.v_scale, self.status)
         self.ws = torch.empty(0, dtype=torch.uint8, device=device)
+        self._outgrown = []  # scratch that a captured graph or another stream may still use
 
     def reserve(self, n_tokens: int, max_q: int, max_seq_len: int = 0) -> None:
         """Scratch for attend() calls of that size; call it before capturing one in a graph."""
         n = rtp_attn_q8_workspace_bytes(self.cfg, self.cache.block_size, n_tokens, max_q, max_seq_len)
         if n > self.ws.numel():
-            self.ws = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+            if self.ws.numel():
+                self._outgrown.append(self.ws)
+            # at least twice the last, so that all outgrown ones together are no larger
+            self.ws = torch.empty(max(n, 2 * self.ws.numel()), dtype=torch.uint8, device=self.k.device)
 
     def append(self, k_pre, v_in, slot_map, pos, stream=None) -> None:
         rtp_append_q8(self.cfg, self.cache, k_pre, v_in, slot_map, pos, self.rope, stream)

@@ -426,7 +426,10 @@ int rtp_append_q8(const rtp_layer_cfg* cfg, const rtp_q8_cache* cache, const voi
                   const int* pos, const rtp_rope_axes* rope, int n_tokens, void* stream);
 
 /* Host.  Scratch bytes of rtp_attn_q8 for calls of up to n_tokens packed
- * queries, max_q of one request and max_seq_len positions (0: cfg->max_ctx). */
+ * queries, max_q of one request and max_seq_len positions (0: cfg->max_ctx).
+ * batch * n_kv_heads * ceil(max_seq_len / 32) * c has to stay below 2^31
+ * (RTP_ERR_SHAPE, here and in rtp_attn_q8); c = ceil(max_q G / 8) for fp32
+ * layers, at most 2 for bf16 ones. */
 int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_tokens, int max_q,
                                 int max_seq_len, size_t* bytes);
 
@@ -438,8 +441,10 @@ int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_
  * window [i - W + 1, i].
  *   out = softmax(RoPE(q, pos) . k_j / sqrt(D)) v_j    k_j, v_j as stored, times their scales
  * One token a request (decode), a few, or chunks, in any mix.  Arithmetic is
- * on tensor cores with fp32 accumulation; queries and softmax weights enter
- * them as fp16 (max_q * G <= 8, and always for fp32 layers: as two fp16 parts).
+ * on tensor cores with fp32 accumulation; queries (scaled by a power of two a
+ * row) and softmax weights enter them as fp16.  Queries enter as two fp16
+ * parts (22 bits) where max_q * G <= 8, and for fp32 layers, whose weights do
+ * so too.  Blocks may be shared between requests.
  *
  *   q_pre        [n_tokens][Hq][D] dtype, device, pre-RoPE; rows q_stride
  *                elements apart (multiple of 16 bytes, at least Hq * D; 0 means Hq * D)

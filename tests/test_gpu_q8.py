@@ -655,6 +655,35 @@ def test_two_streams_with_a_workspace_each():
     b.check(b.out.cpu().double())
 
 
+@pytest.mark.parametrize("new", [[1, 3], [90, 1]])
+def test_requests_that_share_blocks(new):
+    a = _Attn([700, 650], new, bs=32, seed=22)
+    a.table[1, :12] = a.table[0, :12]  # a common prefix of 384 positions
+    a.check(a.run())
+
+
+def test_a_graph_outlives_its_layers_scratch():
+    from synth.workloads import LayerShape
+    sh = LayerShape(batch=2, n_q_heads=8, n_kv_heads=2, head_dim=64, n_sink=4, window=100, top_p=1.0, retrieval=(0,), dtype="bf16")
+    a = _Attn([1900, 400], [1, 1], D=64, seed=23).device()
+    layer = rtp.PagedLayer(sh, a.max_ctx, a.dk.shape[0], a.bs)
+    layer.cache = a.cache
+    layer.reserve(2, 1)
+    small, s, g = layer.ws, torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            layer.attend(a.dq, a.dcu, a.dlen, a.dtab, a.dpos, a.out, 1)
+    layer.reserve(500, 400)
+    assert layer.ws.numel() >= 2 * small.numel() and any(t is small for t in layer._outgrown)
+    filler = torch.full_like(small, 0xFF)  # would lie where the scratch was, had it been freed
+    a.out.fill_(77.0)
+    g.replay()
+    torch.cuda.synchronize()
+    a.check(a.out.cpu().double())
+    assert bool((filler == 0xFF).all())
+
+
 def test_pool_past_two_gigabytes():
     """Blocks at the far end of a 4.5 GB pool: offsets beyond 32 bits, for the append and the attention."""
     nb, hkv, bs, D = 34400, 8, 128, 128

@@ -162,3 +162,16 @@ def test_binding_checks_tensors_before_the_call():
     with pytest.raises(ValueError):  # scales of another shape
         k = torch.zeros(3, 8, 64, 128, dtype=torch.uint8)
         rtp.make_q8_cache(k, k, torch.ones(3, 4), torch.ones(3, 8), torch.zeros(1, dtype=torch.int32))
+
+
+def test_attention_line_stays_below_2_31():
+    # 4096 requests x 8 KV heads x 2^15 tiles of 32 positions: 2^30 a 16-row chunk of queries
+    big = _cfg(batch=4096, max_ctx=1 << 20)
+    rtp.rtp_attn_q8_workspace_bytes(big, 64, 4096, 1)
+    rtp.rtp_attn_q8_workspace_bytes(big, 64, 4096, 4)  # 16 rows
+    _refused(2, rtp.rtp_attn_q8_workspace_bytes, big, 64, 8192, 8)  # 32 rows: two chunks
+    rtp.rtp_attn_q8_workspace_bytes(big, 64, 8192, 8, 1 << 19)
+    _refused(2, _attn, cfg=big, n=8192, max_q=8)
+    fp32 = _cfg(batch=4096, max_ctx=1 << 20, dtype="fp32")
+    rtp.rtp_attn_q8_workspace_bytes(fp32, 64, 4096, 2)  # 8 rows
+    _refused(2, rtp.rtp_attn_q8_workspace_bytes, fp32, 64, 8192, 3)
