@@ -31,7 +31,7 @@ namespace rtp {
 namespace {
 
 constexpr int kAppMaxWarps = 16;
-constexpr int kAppRows = 8;  // rows a warp holds
+constexpr int kAppRows = 8;  // rows a warp of a chunk holds
 
 struct AppQ8Args {
   Q8Pool pool;
@@ -126,18 +126,23 @@ __device__ __forceinline__ float warp_max_positive(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
-template <typename T, int D>
+// A warp holds ST steps of RPS rows: kAppRows for chunks; one step where a
+// request brings a few tokens, since steps without rows are worked on all the
+// same (a decode step of 8 requests: 3.3 us for 5.0).
+constexpr int rows_a_step(int D) { return 32 / (D / 8); }
+
+template <typename T, int D, int ST>
 __global__ void __launch_bounds__(kAppMaxWarps * 32) append_q8_kernel(const __grid_constant__ AppQ8Args a) {
   constexpr int H = D / 2;
-  constexpr int LPR = D / 8;        // lanes a row
-  constexpr int RPS = 32 / LPR;     // rows a step
-  constexpr int ST = kAppRows / RPS;  // steps of a warp's rows
+  constexpr int LPR = D / 8;            // lanes a row
+  constexpr int RPS = rows_a_step(D);
+  constexpr int kRows = ST * RPS;
   __shared__ float s_max[2][kAppMaxWarps][3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int wpr = a.wpr, hpc = nw / wpr, sub = warp % wpr, grp = warp / wpr;
   const int bs = 1 << a.pool.log_bs;
   const long long n_slots = (long long)a.pool.n_blocks << a.pool.log_bs;
-  const int rows_per = wpr * kAppRows;  // rows of a run that a pass holds
+  const int rows_per = wpr * kRows;  // rows of a run that a pass holds
   const int rl = lane / LPR, k0 = (lane % LPR) * 4;  // the lane's row of a step and its first pair
   const int h = blockIdx.y * hpc + grp;
   const bool on = h < a.Hkv;
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kAppMaxWarps * 32) append_q8_kernel(const __gr
       const int passes = (n + rows_per - 1) / rows_per;
       AppPart<T> part[ST] = {};
       float cs[ST][4], sn[ST][4];
-      auto row_of = [&](int p, int st) { return p * rows_per + sub * kAppRows + st * RPS + rl; };
+      auto row_of = [&](int p, int st) { return p * rows_per + sub * kRows + st * RPS + rl; };
       auto key_at = [&](int r) {
         return static_cast<const T*>(a.k_pre) + (size_t)(tl + r) * a.k_stride + (size_t)h * D + k0;
       };
@@ -404,13 +409,15 @@ int launch_append_q8(const Shape& sh, const Q8Pool& pool, const void* k_pre, int
   a.k_pre = k_pre; a.v_in = v_in; a.k_stride = k_stride; a.v_stride = v_stride;
   a.slot = slot_map; a.pos = pos;
   for (int i = 0; i < 64; ++i) a.turns[i] = sh.turns[i];
-  // Steps of a few tokens a request: a warp a run and a CTA for each possible
-  // leader.  Chunks: the warps that hold a whole block, and a
+  // Steps of a few tokens a request: the warps that hold its tokens, and a CTA
+  // for each possible leader.  Chunks: the warps that hold a whole block, and a
   // CTA for each block's worth of tokens.
   const bool step = (long long)n_tokens <= 8ll * sh.B;
   const int bs = 1 << pool.log_bs;
   a.tile = step ? 1 : bs;
-  a.wpr = step ? 1 : bs / kAppRows;
+  a.wpr = bs / kAppRows;
+  if (step)
+    for (a.wpr = 1; (long long)a.wpr * rows_a_step(sh.D) * sh.B < n_tokens;) a.wpr *= 2;  // at most 4
   const int warps = a.wpr > 8 ? a.wpr : 8, hpc = warps / a.wpr;
   const dim3 grid((n_tokens + a.tile - 1) / a.tile, (sh.Hkv + hpc - 1) / hpc);
   cudaLaunchConfig_t cfg = {};
@@ -422,9 +429,15 @@ int launch_append_q8(const Shape& sh, const Q8Pool& pool, const void* k_pre, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void (*k)(AppQ8Args) = sh.dtype == RTP_BF16
-                             ? (sh.D == 128 ? append_q8_kernel<__nv_bfloat16, 128> : append_q8_kernel<__nv_bfloat16, 64>)
-                             : (sh.D == 128 ? append_q8_kernel<float, 128> : append_q8_kernel<float, 64>);
+  void (*k)(AppQ8Args);
+  auto pick = [&](auto few, auto many) { k = step ? few : many; };
+  if (sh.dtype == RTP_BF16) {
+    if (sh.D == 128) pick(append_q8_kernel<__nv_bfloat16, 128, 1>, append_q8_kernel<__nv_bfloat16, 128, kAppRows / rows_a_step(128)>);
+    else pick(append_q8_kernel<__nv_bfloat16, 64, 1>, append_q8_kernel<__nv_bfloat16, 64, kAppRows / rows_a_step(64)>);
+  } else {
+    if (sh.D == 128) pick(append_q8_kernel<float, 128, 1>, append_q8_kernel<float, 128, kAppRows / rows_a_step(128)>);
+    else pick(append_q8_kernel<float, 64, 1>, append_q8_kernel<float, 64, kAppRows / rows_a_step(64)>);
+  }
   trace_begin(RTP_STAGE_APPEND_Q8, st);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
   trace_end(RTP_STAGE_APPEND_Q8, st);

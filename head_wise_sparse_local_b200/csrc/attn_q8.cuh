@@ -43,7 +43,7 @@ struct __align__(64) AttnQ8Args {
   unsigned long long wait_ns;
   // the chunk kernel's share of the workspace
   ChunkItem* items;
-  long long* prefix;  // tiles ahead of each item, then their number; [max_chunk_items + 1]: a CTA's share of them
+  long long* prefix;  // units of the line ahead of each item, then their number; [max_chunk_items + 1]: a CTA's share of them
   int* req_items;     // [B + 1] items ahead of each request
   float* cpart;       // partials of cut items: [2 CTAs][256][D], and (M, l)
   float* cpart_ml;

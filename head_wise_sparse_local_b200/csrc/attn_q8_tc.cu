@@ -10,20 +10,22 @@
 // Work.  An item is 256 query rows of one (request, KV head): row r is token
 // r / G, query head r % G of the group, so the G heads share every tile of K
 // and V and a chunk of 64 G-head tokens fills the tensor cores' rows.  A tile
-// is 128 positions.  The tiles of all items form one line that is cut into equal
-// shares, one a CTA (one an SM): causal triangles, windows and ragged batches
-// load the SMs evenly.  A cut item leaves partials that a second kernel joins.  A first,
-// one-CTA kernel lays the line out.
+// is 128 positions.  The tiles of all items, and three more units an item for its
+// start and end (without them the CTAs with many short window items finished a
+// tenth late: 418 us for 384), form one line that is cut into equal shares, one
+// a CTA (one an SM): causal triangles, windows and ragged batches load the SMs
+// evenly.  A cut item leaves partials that a last kernel joins.
 //
 // Roles (16 warps):
 //   warps 0-3, 4-7   the softmax of slot 0 and slot 1 (128 rows each), one
-//                    thread a row: weights against the running maximum as S is
-//                    read from TMEM, written over the columns already read;
-//                    where 32 columns exceed the maximum by 2^9, it moves, and O
-//                    and the tile's weights so far are rescaled (holding
-//                    the row in registers to find its maximum first took
-//                    straight-line code that the instruction cache could not
-//                    feed: 8100 clocks a tile; reading S twice, 5650);
+//                    thread a row: 64 columns of S at a time are read from TMEM
+//                    and their fp16 weights against the running maximum written
+//                    over columns already read; where they exceed the maximum by
+//                    2^9, it moves, and O and the tile's weights so far are
+//                    rescaled.  One rolled loop: the same in straight-line code
+//                    for 4 x 32 columns took 475 us for the 418 (the instruction
+//                    cache could not feed it), a rolled loop over 32 columns 409
+//                    for 384, whole rows in registers and S read twice more still;
 //   warps 8-11       convert a tile's e4m3 rows to fp16 in the operands' swizzled layout;
 //   warp 12          issues the products in the order S0(i), PV1(i-1), S1(i),
 //                    PV0(i): each slot's softmax runs beside the other's products;
@@ -32,16 +34,25 @@
 // The roles run on from item to item on their own; nothing synchronises the CTA
 // between its first and its last tile.
 //
-// The first kernel also rotates the queries: fp16 rows and their scales, once
-// a token, not once a CTA in a prologue that stalls its products (33000 clocks an
-// item, measured).
+// The first kernel lays the line out and rotates the queries: fp16 rows and
+// their scales, once a token, not once a CTA in a prologue that stalls its
+// products (33000 clocks an item, measured).
 //
 // Every wait is bounded: on expiry the CTA sets RTP_DEV_TIMEOUT, stops issuing,
 // waits (bounded) for what it issued and frees its TMEM.
 //
 // Bound: the tensor cores.  A tile of 256 x 128 pairs at D = 128 is 16.8 MFLOP,
 // 2048 clocks at the dense fp16 rate; its weights are 32768 exponentials, 2048
-// clocks of the MUFU pipe, of which a quarter go to the FMA pipe.
+// clocks of the MUFU pipe, of which a quarter go to the FMA pipe (none: 399 us
+// for 384; an eighth 393; a half 421).
+//
+// Measured, 2K queries of 32 heads at 32K positions, D = 128: 384 us (319 GFLOP,
+// 830 TFLOP/s, half of a large matrix product's rate).  A tile takes 4950 clocks: a
+// slot's softmax 2700 of them, then its own two products and the turn of the
+// other slot's (1700), 250 from one to the next; an item's end and start 15000.
+// Halves of a tile with their own products, so that a slot's softmax need not
+// wait for them, made the products' issue the bound instead (64-column products
+// are 48 clocks for half the work of 64.5): 411 us.
 #include <mutex>
 
 #include "attn_q8.cuh"
@@ -126,7 +137,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long& total, l
 }
 
 // Block 0 lays out the line: items in the order (request, KV head, group), and
-// the tiles ahead of each.  The others rotate queries: a warp a token and 8
+// the units ahead of each.  The others rotate queries: a warp a token and 8
 // heads; every row becomes fp16 of its power-of-two scale, and its factor from
 // products to base-2 logits.
 template <int D>
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
   if (flags) atomicOr(a.pool.status, flags);
 }
 
-// The item whose tiles hold line position `at` (one warp; prefix[n] > at).
+// The item whose units hold line position `at` (one warp; prefix[n] > at).
 __device__ __forceinline__ int find_item(const long long* prefix, int n, long long at) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = n;  // the answer is in [lo, lo + len)
