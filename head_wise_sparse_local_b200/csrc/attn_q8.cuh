@@ -45,7 +45,7 @@ struct __align__(64) AttnQ8Args {
   ChunkItem* items;
   long long* prefix;  // units of the line ahead of each item, then their number; [max_chunk_items + 1]: a CTA's share of them
   int* req_items;     // [B + 1] items ahead of each request
-  float* cpart;       // partials of cut items: [2 CTAs][256][D], and (M, l)
+  float* cpart;       // partials of cut items: [2 CTAs][D / 4][256][4], and (M, l)
   float* cpart_ml;
   int max_chunk_items;
   __half* cq;         // rotated queries, [n_tokens][Hq][D], each row by its power-of-two scale

@@ -144,6 +144,8 @@ template <int D>
 __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constant__ AttnQ8Args a) {
   if (blockIdx.x > 0) {
     constexpr int PP = D / 64, H = D / 2;
+    struct __align__(2 * PP) Pairs { __nv_bfloat16 x[PP]; };  // a lane's dims, below H or from H on
+    struct __align__(2 * PP) Halves { __half x[PP]; };
     const int lane = threadIdx.x & 31;
     const int hb = (a.Hq + 7) / 8;
     const long long task = (long long)(blockIdx.x - 1) * (kCPrep / 32) + (threadIdx.x >> 5);
@@ -164,10 +166,11 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
 #pragma unroll
     for (int h = 0; h < 8; ++h)
       if (h < nh) {
+        const Pairs u = *reinterpret_cast<const Pairs*>(q + h * D), v = *reinterpret_cast<const Pairs*>(q + h * D + H);
 #pragma unroll
         for (int i = 0; i < PP; ++i) {
-          x1[h][i] = to_f32(q[h * D + i]);
-          x2[h][i] = to_f32(q[h * D + H + i]);
+          x1[h][i] = to_f32(u.x[i]);
+          x2[h][i] = to_f32(v.x[i]);
         }
       }
 #pragma unroll
@@ -184,11 +187,14 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
       const float sc = query_scale(warp_max(m)), inv = 1.f / sc;
       const size_t row = (size_t)t * a.Hq + h0 + h;
       __half* o = a.cq + row * D + lane * PP;
+      Halves y1, y2;
 #pragma unroll
       for (int i = 0; i < PP; ++i) {
-        o[i] = __float2half_rn(x1[h][i] * inv);
-        o[H + i] = __float2half_rn(x2[h][i] * inv);
+        y1.x[i] = __float2half_rn(x1[h][i] * inv);
+        y2.x[i] = __float2half_rn(x2[h][i] * inv);
       }
+      *reinterpret_cast<Halves*>(o) = y1;
+      *reinterpret_cast<Halves*>(o + H) = y2;
       if (lane == 0) a.cq_unit[row] = sc * unit;
     }
     return;
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
       if (poison) l = CUDART_NAN_F;
       const bool alone = w.u0 == 0 && w.nt == c.tiles;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D;
-      const size_t prow = (size_t)(2 * blockIdx.x + (w.u0 > 0 ? 0 : 1)) * kCGroup + r;
+      const size_t pn = (size_t)(2 * blockIdx.x + (w.u0 > 0 ? 0 : 1));  // the partial: four dims of all rows lie together
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {
@@ -608,10 +614,11 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
         } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(a.cpart + prow * D + k * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            *reinterpret_cast<float4*>(a.cpart + ((pn * (D / 4) + k * 8 + e / 4) * kCGroup + r) * 4) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-      if (rv && !alone) *reinterpret_cast<float2*>(a.cpart_ml + prow * 2) = make_float2(M, l);
+      if (rv && !alone) *reinterpret_cast<float2*>(a.cpart_ml + (pn * kCGroup + r) * 2) = make_float2(M, l);
       tc_fence_before();
       mbar_arrive(&bars.o_empty[slot]);
       ++seg;
@@ -816,7 +823,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
 // is the cut ahead of share x + 1, and works if it is its item's first.
 template <int D>
 __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_constant__ AttnQ8Args a) {
-  constexpr int LPR = D / 4;  // threads a row
+  constexpr int kRows = 64;  // of a CTA, by 16 dims
   griddep_wait();
   const int n_items = a.req_items[a.B];
   const long long total = a.prefix[n_items], share = a.prefix[a.max_chunk_items + 1];
@@ -829,19 +836,19 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
   const ChunkItem c = a.items[item];
   if (at - first >= c.tiles) return;
   const int c1 = (int)((first + c.tiles - 1) / share);
-  const int r = blockIdx.y * (256 / LPR) + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
+  const int r = (blockIdx.y & 3) * kRows + (threadIdx.x & 63), d4 = (blockIdx.y >> 2) * 4 + (threadIdx.x >> 6);
   if (r >= c.n_rows) return;
   // the share that starts the item keeps its partial second, the later ones first
-  auto row = [&](int k) { return (size_t)(k == cut - 1 ? 2 * k + 1 : 2 * k) * kCGroup + r; };
+  auto part = [&](int k) { return (size_t)(k == cut - 1 ? 2 * k + 1 : 2 * k); };
   float m = -CUDART_INF_F;
-  for (int k = cut - 1; k <= c1; ++k) m = fmaxf(m, a.cpart_ml[row(k) * 2]);
+  for (int k = cut - 1; k <= c1; ++k) m = fmaxf(m, a.cpart_ml[(part(k) * kCGroup + r) * 2]);
   const float ms = m == -CUDART_INF_F ? 0.f : m;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
 #pragma unroll 2
   for (int k = cut - 1; k <= c1; ++k) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.cpart_ml + row(k) * 2);
-    const float4 p = *reinterpret_cast<const float4*>(a.cpart + row(k) * D + d);
+    const float2 ml = *reinterpret_cast<const float2*>(a.cpart_ml + (part(k) * kCGroup + r) * 2);
+    const float4 p = *reinterpret_cast<const float4*>(a.cpart + ((part(k) * (D / 4) + d4) * kCGroup + r) * 4);
     const float f = ex2(ml.x - ms);
     l = fmaf(ml.y, f, l);
     o.x = fmaf(p.x, f, o.x);
@@ -854,7 +861,7 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
   uint2 v;
   v.x = pack_bf16(o.x * inv, o.y * inv);
   v.y = pack_bf16(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D + d) = v;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D + d4 * 4) = v;
 }
 
 long long max_chunk_items(const Shape& sh, int n_tokens, int max_q, int small) {
