@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
     return;
   }
   __shared__ long long s_warp[kCPrep / 32];
+  __shared__ int s_req[kCPrep];  // req_items, where they fit
   griddep_wait();
   griddep_launch();
   int flags = 0;
@@ -214,12 +215,13 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
     }
     long long total;
     const long long x = n_items + block_scan(v, total, s_warp);
-    if (b < a.B) a.req_items[b] = (int)min(x, (long long)a.max_chunk_items);
+    if (b < a.B) s_req[threadIdx.x] = a.req_items[b] = (int)min(x, (long long)a.max_chunk_items);
     n_items += total;
   }
   n_items = min(n_items, (long long)a.max_chunk_items);  // more only if cu_q goes back and forth
   if (threadIdx.x == 0) a.req_items[a.B] = (int)n_items;
   __syncthreads();
+  const int* req = a.B <= kCPrep ? s_req : a.req_items;
   long long tiles = 0;
   for (int i0 = 0; i0 < n_items; i0 += kCPrep) {
     const int i = i0 + threadIdx.x;
@@ -229,11 +231,11 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
       int b = 0, hi = a.B;  // the last request with req_items <= i
       while (hi - b > 1) {
         const int mid = (b + hi) >> 1;
-        if (a.req_items[mid] <= i) b = mid;
+        if (req[mid] <= i) b = mid;
         else hi = mid;
       }
       const ReqRows r = load_rows(a, b, flags);
-      const int ng = (r.n * a.G + kCGroup - 1) / kCGroup, rel = i - a.req_items[b];
+      const int ng = (r.n * a.G + kCGroup - 1) / kCGroup, rel = i - req[b];
       it = chunk_item(a, r, b, rel / ng, rel % ng);
       v = it.tiles + kCItemCost;
     }
@@ -823,7 +825,9 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
 // is the cut ahead of share x + 1, and works if it is its item's first.
 template <int D>
 __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_constant__ AttnQ8Args a) {
-  constexpr int kRows = 64;  // of a CTA, by 16 dims
+  // a CTA takes 64 rows and half the dims, a thread J times four of them: the chain of loads
+  // that finds the item and its weights is walked once
+  constexpr int kRows = 64, J = D / 32;
   griddep_wait();
   const int n_items = a.req_items[a.B];
   const long long total = a.prefix[n_items], share = a.prefix[a.max_chunk_items + 1];
@@ -836,32 +840,45 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
   const ChunkItem c = a.items[item];
   if (at - first >= c.tiles) return;
   const int c1 = (int)((first + c.tiles - 1) / share);
-  const int r = (blockIdx.y & 3) * kRows + (threadIdx.x & 63), d4 = (blockIdx.y >> 2) * 4 + (threadIdx.x >> 6);
+  const int r = (blockIdx.y & 3) * kRows + (threadIdx.x & 63), d4 = (blockIdx.y >> 2) * (D / 8) + (threadIdx.x >> 6) * J;
   if (r >= c.n_rows) return;
   // the share that starts the item keeps its partial second, the later ones first
   auto part = [&](int k) { return (size_t)(k == cut - 1 ? 2 * k + 1 : 2 * k); };
   float m = -CUDART_INF_F;
   for (int k = cut - 1; k <= c1; ++k) m = fmaxf(m, a.cpart_ml[(part(k) * kCGroup + r) * 2]);
   const float ms = m == -CUDART_INF_F ? 0.f : m;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 o[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
 #pragma unroll 2
   for (int k = cut - 1; k <= c1; ++k) {
     const float2 ml = *reinterpret_cast<const float2*>(a.cpart_ml + (part(k) * kCGroup + r) * 2);
-    const float4 p = *reinterpret_cast<const float4*>(a.cpart + ((part(k) * (D / 4) + d4) * kCGroup + r) * 4);
+    float4 p[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) p[j] = *reinterpret_cast<const float4*>(a.cpart + ((part(k) * (D / 4) + d4 + j) * kCGroup + r) * 4);
     const float f = ex2(ml.x - ms);
     l = fmaf(ml.y, f, l);
-    o.x = fmaf(p.x, f, o.x);
-    o.y = fmaf(p.y, f, o.y);
-    o.z = fmaf(p.z, f, o.z);
-    o.w = fmaf(p.w, f, o.w);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      o[j].x = fmaf(p[j].x, f, o[j].x);
+      o[j].y = fmaf(p[j].y, f, o[j].y);
+      o[j].z = fmaf(p[j].z, f, o[j].z);
+      o[j].w = fmaf(p[j].w, f, o[j].w);
+    }
   }
   const int tok = c.q0 + ((c.row0 + r) >> a.log_g), hq = c.h * a.G + ((c.row0 + r) & (a.G - 1));
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint2 v;
-  v.x = pack_bf16(o.x * inv, o.y * inv);
-  v.y = pack_bf16(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D + d4 * 4) = v;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D + d4 * 4;
+#pragma unroll
+  for (int j = 0; j < J; j += 2) {
+    uint4 v;
+    v.x = pack_bf16(o[j].x * inv, o[j].y * inv);
+    v.y = pack_bf16(o[j].z * inv, o[j].w * inv);
+    v.z = pack_bf16(o[j + 1].x * inv, o[j + 1].y * inv);
+    v.w = pack_bf16(o[j + 1].z * inv, o[j + 1].w * inv);
+    *reinterpret_cast<uint4*>(out + j * 4) = v;
+  }
 }
 
 long long max_chunk_items(const Shape& sh, int n_tokens, int max_q, int small) {
@@ -910,7 +927,7 @@ cudaError_t launch_chunks(const AttnQ8Args& a, cudaStream_t st) {
   e = launch_pdl(chunk_prep_kernel<D>, dim3((unsigned)(1 + (tasks + kCPrep / 32 - 1) / (kCPrep / 32))), dim3(kCPrep), 0, st, a);
   if (e == cudaSuccess) e = launch_pdl(attn_q8_chunk_kernel<D>, dim3(kCCtas), dim3(kCThreads), CSmem<D>::kBytes, st, a);
   if (e == cudaSuccess)
-    e = launch_pdl(attn_q8_chunk_join_kernel<D>, dim3(kCCtas - 1, kCGroup * (D / 4) / 256), dim3(256), 0, st, a);
+    e = launch_pdl(attn_q8_chunk_join_kernel<D>, dim3(kCCtas - 1, 2 * kCGroup / 64), dim3(256), 0, st, a);
   return e;
 }
 
