@@ -147,12 +147,20 @@ __global__ void __launch_bounds__(kAppMaxWarps * 32) append_q8_kernel(const __gr
   const int h = blockIdx.y * hpc + grp;
   const bool on = h < a.Hkv;
   const bool axes = a.rope.n_axes > 1;
-  uint64_t turns[4];  // of the lane's pairs (lanes that index the parameters apart are served one by one: once a kernel)
+  // lanes that index the parameters apart are served one by one: once a CTA
+  __shared__ uint64_t s_turns[H];
+  __shared__ int s_axis[H];
+  for (int k = tid; k < H; k += blockDim.x) {
+    s_turns[k] = a.turns[k];
+    s_axis[k] = axes ? a.rope.axis[k] : 0;
+  }
+  __syncthreads();
+  uint64_t turns[4];  // of the lane's pairs
   int axis[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    turns[e] = a.turns[k0 + e];
-    axis[e] = axes ? a.rope.axis[k0 + e] : 0;
+    turns[e] = s_turns[k0 + e];
+    axis[e] = s_axis[k0 + e];
   }
   griddep_wait();
   griddep_launch();
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kAppMaxWarps * 32) append_q8_kernel(const __gr
         return static_cast<const T*>(a.k_pre) + (size_t)(tl + r) * a.k_stride + (size_t)h * D + k0;
       };
       auto pos_at = [&](int r, int k) {
-        return a.pos[(size_t)(tl + r) + (axes ? (size_t)a.rope.axis[k] * a.n_tokens : 0)];
+        return a.pos[(size_t)(tl + r) + (size_t)s_axis[k] * a.n_tokens];
       };
       auto load = [&](int p) {  // a pass's rows, and the cosines of their positions
 #pragma unroll
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(kAppMaxWarps * 32) append_q8_kernel(const __gr
             if (!mine || !on || r >= n || (bad >> st & 1u)) continue;
 #pragma unroll 1
             for (int e = 0; e < 4; ++e) {
-              const float2 y = exact_pair(to_f32(key_at(r)[e]), to_f32(key_at(r)[e + H]), pos_at(r, k0 + e), a.turns[k0 + e]);
+              const float2 y = exact_pair(to_f32(key_at(r)[e]), to_f32(key_at(r)[e + H]), pos_at(r, k0 + e), s_turns[k0 + e]);
               m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
             }
           }
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(kAppMaxWarps * 32) append_q8_kernel(const __gr
           off_by = lv && !bd ? off_by : 0u;
           while (off_by) {  // pair i lies too near a border
             const int i = (__ffs(off_by) - 1) >> 3;
-            const float2 x = exact_pair(to_f32(key_at(r)[i]), to_f32(key_at(r)[i + H]), pos_at(r, k0 + i), a.turns[k0 + i]);
+            const float2 x = exact_pair(to_f32(key_at(r)[i]), to_f32(key_at(r)[i + H]), pos_at(r, k0 + i), s_turns[k0 + i]);
             const uint32_t z = f32x2_to_e4m3x2(x.x * ki, x.y * ki);
             q1 = (q1 & ~(0xffu << (8 * i))) | (z & 0xffu) << (8 * i);
             q2 = (q2 & ~(0xffu << (8 * i))) | (z >> 8) << (8 * i);

@@ -201,6 +201,8 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
   __shared__ __align__(8) uint64_t s_bar[kAqWarps][kAqStages];
   __shared__ float s_qs[ROWS];  // per row: factor from products to base-2 logits
   __shared__ int s_abort;
+  __shared__ uint64_t s_turns[D / 2];  // (lanes that index the parameters apart are served one by one)
+  __shared__ int s_axis[D / 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   unsigned char* dsm = dsm_raw + ((1024u - (smem_u32(dsm_raw) & 1023u)) & 1023u);
@@ -213,6 +215,10 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     for (int w = 0; w < kAqWarps; ++w)
       for (int s = 0; s < kAqStages; ++s) mbar_init(&s_bar[w][s], 2);
     s_abort = 0;
+  }
+  if (tid < D / 2) {
+    s_turns[tid] = a.turns[tid];
+    s_axis[tid] = a.rope.n_axes > 1 ? a.rope.axis[tid] : 0;
   }
   __syncthreads();
   griddep_wait();
@@ -308,8 +314,8 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     };
     auto load_pair = [&](int task, Pair& y) {
       const int tl = task / (D / 2), k = task % (D / 2), tok = rq.q0 + tok0 + tl;
-      y.turns = a.turns[k];
-      y.pos = a.c.pos[(size_t)(a.rope.n_axes > 1 ? a.rope.axis[k] : 0) * a.c.n_tokens + tok];
+      y.turns = s_turns[k];
+      y.pos = a.c.pos[(size_t)s_axis[k] * a.c.n_tokens + tok];
       y.ra = max(((tok0 + tl) << a.log_g) - row0, 0);
       y.rb = min(((tok0 + tl + 1) << a.log_g) - row0, n_rows);
       const T* q = static_cast<const T*>(a.c.q_pre) + (size_t)tok * a.c.q_stride +

@@ -149,6 +149,14 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
     const int lane = threadIdx.x & 31;
     const int hb = (a.Hq + 7) / 8;
     const long long task = (long long)(blockIdx.x - 1) * (kCPrep / 32) + (threadIdx.x >> 5);
+    // lanes that index the parameters apart are served one by one: once a CTA, not once a warp
+    __shared__ uint64_t s_turns[H];
+    __shared__ int s_axis[H];
+    if (threadIdx.x < H) {
+      s_turns[threadIdx.x] = a.turns[threadIdx.x];
+      s_axis[threadIdx.x] = a.rope.axis[threadIdx.x];
+    }
+    __syncthreads();
     griddep_wait();
     griddep_launch();
     if (task >= (long long)a.c.n_tokens * hb) return;
@@ -158,7 +166,7 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < PP; ++i) {
       const int k = lane * PP + i;
-      rope_turns(a.c.pos[(size_t)a.rope.axis[k] * a.c.n_tokens + t], a.turns[k], c[i], s[i]);
+      rope_turns(a.c.pos[(size_t)s_axis[k] * a.c.n_tokens + t], s_turns[k], c[i], s[i]);
     }
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.c.q_pre) + (size_t)t * a.c.q_stride + (size_t)h0 * D + lane * PP;
     const int nh = min(a.Hq - h0, 8);
