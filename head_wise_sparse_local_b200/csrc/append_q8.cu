@@ -424,8 +424,16 @@ int launch_append_q8(const Shape& sh, const Q8Pool& pool, const void* k_pre, int
   const int bs = 1 << pool.log_bs;
   a.tile = step ? 1 : bs;
   a.wpr = bs / kAppRows;
-  if (step)
-    for (a.wpr = 1; (long long)a.wpr * rows_a_step(sh.D) * sh.B < n_tokens;) a.wpr *= 2;  // at most 4
+  if (step && n_tokens == sh.B) {
+    a.wpr = 1;  // a token each
+  } else if (step) {
+    // any one request may bring a whole block: two warps a run at least, more while the CTAs are few
+    // (200 tokens of one of 256 requests: 31 us with 8 rows a warp, 39 with one warp of 2, 20 with two;
+    // 256 requests of a token each 4.2 with one warp, 6.8 with two, 12.5 with four)
+    for (a.wpr = 2; a.wpr < 8 && ((long long)a.wpr * rows_a_step(sh.D) * sh.B < n_tokens ||
+                                  2ll * a.wpr * n_tokens * sh.Hkv <= 8 * 512);)
+      a.wpr *= 2;
+  }
   // eight warps at least, but none for heads that the layer has not got (they
   // do the work all the same: 10.1 for 9.3 us on a 2-head layer)
   const int hpc = a.wpr >= 8 ? 1 : 8 / a.wpr < sh.Hkv ? 8 / a.wpr : sh.Hkv, warps = hpc * a.wpr;

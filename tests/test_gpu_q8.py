@@ -290,6 +290,29 @@ def test_append_slices_of_the_fused_projection():
     h.check()
 
 
+@pytest.mark.parametrize("dtype,D,hkv,bs,B,runs", [
+    ("bf16", 128, 1, 64, 4, [1, 1, 1, 1]),           # one head, a token each: a CTA of one warp
+    ("fp32", 128, 1, 16, 3, [1, 2, 1]),
+    ("bf16", 64, 2, 128, 200, [200]),                 # as many tokens as requests, but one brings them all
+    ("bf16", 128, 2, 64, 300, [200]),
+    ("fp32", 64, 3, 32, 60, [1] * 59 + [400]),
+    ("bf16", 128, 8, 16, 16, [4] * 16),
+    ("bf16", 64, 64, 16, 2, [1, 1]),
+])
+def test_append_steps_of_any_shape(dtype, D, hkv, bs, B, runs):
+    gen = _gen(len(runs) + D)
+    blocks = [-(-(3 + n) // bs) for n in runs]  # every run starts at a block's row 3
+    h = _Held(sum(blocks), hkv, bs, D, dtype, G=1, B=B)
+    first = np.concatenate([[0], np.cumsum(blocks)])
+    slots = [int(first[i]) * bs + 3 + t for i, n in enumerate(runs) for t in range(n)]
+    N = len(slots)
+    assert N <= 8 * B
+    for scale in (1.0, 30.0):  # the second call writes over the first and grows the scales
+        h.append((torch.randn(N, hkv, D, generator=gen) * scale).to(h.dt), torch.randn(N, hkv, D, generator=gen).to(h.dt), slots,
+                 h.positions(N, gen))
+        h.check()
+
+
 def test_append_big_step_of_many_requests():
     """More runs than SMs, one token each, and heads that fill no warp group evenly."""
     gen = _gen(7)
