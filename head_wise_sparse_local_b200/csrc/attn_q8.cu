@@ -34,6 +34,11 @@
 // 23 B a clock, so 1400 clocks; the products are 192 mma.sync of 2 clocks each and 512
 // conversions of about 1 clock.  (tcgen05 would spend as long: its 128-row operand would be
 // 8 or 16 rows full.)
+//
+// Measured, 32 query / 8 KV heads, D = 128, bf16, both kernels of a call: one
+// request at 1M positions 92 us (543 MB, 5.9 TB/s, 90% of a copy's rate), at 128K
+// 22 us (70 MB); 8 requests of 8K to 32K positions 27 us (95 MB), with four or five
+// queries each 42 us (16 rows a chunk, so their tiles are read twice).
 #include "attn_q8.cuh"
 #include "tensor_map.h"
 

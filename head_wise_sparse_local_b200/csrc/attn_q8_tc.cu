@@ -46,10 +46,11 @@
 // clocks of the MUFU pipe, of which a quarter go to the FMA pipe (none: 399 us
 // for 384; an eighth 393; a half 421).
 //
-// Measured, 2K queries of 32 heads at 32K positions, D = 128: 384 us (319 GFLOP,
-// 830 TFLOP/s, half of a large matrix product's rate).  A tile takes 4950 clocks: a
-// slot's softmax 2700 of them, then its own two products and the turn of the
-// other slot's (1700), 250 from one to the next; an item's end and start 15000.
+// Measured, 2K queries of 32 heads at 32K positions, D = 128: 365 us for the
+// three kernels (319 GFLOP, 870 TFLOP/s, 53% of a large matrix product's rate).
+// A tile takes 4950 clocks: a slot's softmax 2700 of them, then its own two
+// products and the turn of the other slot's (1700), 250 from one to the next;
+// an item's end and start about as long as three tiles.
 // Halves of a tile with their own products, so that a slot's softmax need not
 // wait for them, made the products' issue the bound instead (64-column products
 // are 48 clocks for half the work of 64.5): 411 us.
