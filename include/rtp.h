@@ -444,7 +444,8 @@ int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_
  * on tensor cores with fp32 accumulation; queries (scaled by a power of two a
  * row) and softmax weights enter them as fp16.  Queries enter as two fp16
  * parts (22 bits) where max_q * G <= 8, and for fp32 layers, whose weights do
- * so too.  Blocks may be shared between requests.
+ * so too.  Blocks may be shared between requests.  v holds no NaN at cached
+ * positions (rtp_append_q8 writes none): a weight of 0 does not hide one.
  *
  *   q_pre        [n_tokens][Hq][D] dtype, device, pre-RoPE; rows q_stride
  *                elements apart (multiple of 16 bytes, at least Hq * D; 0 means Hq * D)
