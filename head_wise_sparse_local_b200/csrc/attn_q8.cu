@@ -82,9 +82,11 @@ __device__ __forceinline__ ReqQ8 load_req(const AttnQ8Args& a, int b, int& flags
   return r;
 }
 
-// Tiles a CTA takes: an equal share of the line, at least one a warp.
-__device__ __forceinline__ uint32_t share_of(uint32_t total) {
-  return max((total + kAqMaxCtas - 1) / kAqMaxCtas, (uint32_t)kAqWarps);
+// Tiles a CTA takes: an equal share of the line, at least one a warp, or the
+// items' mean where that is less (short contexts: four one-tile items after one
+// another took 16 us where a CTA each takes 7).
+__device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t items) {
+  return max((total + kAqMaxCtas - 1) / kAqMaxCtas, min((uint32_t)kAqWarps, total / max(items, 1u)));
 }
 
 // Where position `part` * share of the line lies (every warp for itself): its
@@ -108,12 +110,14 @@ __device__ __forceinline__ LineAt locate(const AttnQ8Args& a, uint32_t part, int
   uint32_t t, it, ts, is;
   sums(0, t, it, ts, is);
   p.total = __shfl_sync(0xffffffffu, ts, 31);
+  uint32_t all_items = __shfl_sync(0xffffffffu, is, 31);
   for (int b0 = 32; b0 < a.B; b0 += 32) {
     uint32_t t2, it2, ts2, is2;
     sums(b0, t2, it2, ts2, is2);
     p.total += __shfl_sync(0xffffffffu, ts2, 31);
+    all_items += __shfl_sync(0xffffffffu, is2, 31);
   }
-  p.share = share_of(p.total);
+  p.share = share_of(p.total, all_items);
   p.at = part * p.share;
   if (p.at >= p.total) return p;
   for (int b0 = 0;;) {
