@@ -11,9 +11,9 @@
 // maximum of x, moved only when a tile exceeds it by 2^8.
 //
 // Work.  A tile is 32 positions of one (request, KV head, row chunk) item.  All
-// tiles of all items form one line that is cut into equal shares, one for
-// each CTA (two an SM), so ragged batches and the short local heads load the
-// SMs evenly; an item that a cut goes through leaves one partial (O, M, l) a
+// tiles of all items, and some units an item for its start and end, form one
+// line that is cut into equal shares, one for each CTA (two an SM), so ragged
+// batches and the short local heads load the SMs evenly; an item that a cut goes through leaves one partial (O, M, l) a
 // CTA, and a second kernel joins them in order, from a note that the item's
 // first CTA leaves it (finding the items anew cost it 4 us at 128K; a join by
 // the CTA that arrives last, counted by compare-and-swap so that the workspace
@@ -37,8 +37,8 @@
 //
 // Measured, 32 query / 8 KV heads, D = 128, bf16, both kernels of a call: one
 // request at 1M positions 92 us (543 MB, 5.9 TB/s, 90% of a copy's rate), at 128K
-// 22 us (70 MB); 8 requests of 8K to 32K positions 27 us (95 MB), with four or five
-// queries each 42 us (16 rows a chunk, so their tiles are read twice).
+// 21 us (70 MB); 8 requests of 8K to 32K positions 24 us (95 MB), as drafts 39 us
+// (16 rows a chunk, so their tiles are read twice).
 #include "attn_q8.cuh"
 #include "tensor_map.h"
 
@@ -49,6 +49,10 @@ constexpr int kAqWarps = 4;
 constexpr int kAqThreads = kAqWarps * 32;
 constexpr int kAqTile = 32;   // positions a tile
 constexpr int kAqStages = 3;  // tiles in flight a warp
+// Units of the line after an item's tiles: its start and end cost about as much as so many
+// tiles (none: 27.2 us for 8 requests of 8K to 32K, 43.1 for drafts there; 8: 25.1 and 40.8;
+// 16: 24.2 and 38.6; 28: 25.4 and 39.6).
+constexpr int kAqItemCost = 16;
 constexpr int kAqCtasPerSm = 2;
 constexpr int kAqMaxCtas = 148 * kAqCtasPerSm;  // every SM of a B200
 
@@ -58,7 +62,9 @@ struct ReqQ8 {
   int rc;         // row chunks
   int tr, tl;     // tiles of a retrieval and of a local KV head
   int ns, w0;     // a local head's tiles: [0, ns) and [w0, tr)
-  __device__ __forceinline__ uint32_t tiles(int R, int Hkv) const { return (uint32_t)rc * (uint32_t)(R * tr + (Hkv - R) * tl); }
+  __device__ __forceinline__ uint32_t units(int R, int Hkv) const {  // of the line
+    return (uint32_t)rc * (uint32_t)(R * tr + (Hkv - R) * tl + Hkv * kAqItemCost);
+  }
 };
 
 __device__ __forceinline__ ReqQ8 load_req(const AttnQ8Args& a, int b, int& flags) {
@@ -82,18 +88,18 @@ __device__ __forceinline__ ReqQ8 load_req(const AttnQ8Args& a, int b, int& flags
   return r;
 }
 
-// Tiles a CTA takes: an equal share of the line, at least one a warp, or the
+// Units a CTA takes: an equal share of the line, at least one a warp, or the
 // items' mean where that is less (short contexts: four one-tile items after one
 // another took 16 us where a CTA each takes 7).
 __device__ __forceinline__ uint32_t share_of(uint32_t total, uint32_t items) {
-  return max((total + kAqMaxCtas - 1) / kAqMaxCtas, min((uint32_t)kAqWarps, total / max(items, 1u)));
+  return max((total + kAqMaxCtas - 1) / kAqMaxCtas, min((uint32_t)kAqWarps, total / max(items, 1u) - kAqItemCost));
 }
 
 // Where position `part` * share of the line lies (every warp for itself): its
-// request, and the tiles and items ahead of that.  b < 0: past the end.
+// request, and the units and items ahead of that.  b < 0: past the end.
 struct LineAt {
   int b;
-  uint32_t at, share, total, tiles, items;
+  uint32_t at, share, total, units, items;
 };
 
 __device__ __forceinline__ LineAt locate(const AttnQ8Args& a, uint32_t part, int& flags) {
@@ -102,7 +108,7 @@ __device__ __forceinline__ LineAt locate(const AttnQ8Args& a, uint32_t part, int
   auto sums = [&](int b0, uint32_t& t, uint32_t& it, uint32_t& ts, uint32_t& is) {
     ReqQ8 r = {};
     if (b0 + lane < a.B) r = load_req(a, b0 + lane, flags);
-    t = r.tiles(R, a.Hkv);
+    t = r.units(R, a.Hkv);
     it = (uint32_t)(r.rc * a.Hkv);
     ts = warp_incl_scan_u32(t);
     is = warp_incl_scan_u32(it);
@@ -121,23 +127,23 @@ __device__ __forceinline__ LineAt locate(const AttnQ8Args& a, uint32_t part, int
   p.at = part * p.share;
   if (p.at >= p.total) return p;
   for (int b0 = 0;;) {
-    const unsigned m = __ballot_sync(0xffffffffu, p.tiles + ts > p.at);
+    const unsigned m = __ballot_sync(0xffffffffu, p.units + ts > p.at);
     if (m) {
       const int l = __ffs(m) - 1;
       p.b = b0 + l;
-      p.tiles += __shfl_sync(0xffffffffu, ts - t, l);
+      p.units += __shfl_sync(0xffffffffu, ts - t, l);
       p.items += __shfl_sync(0xffffffffu, is - it, l);
       return p;
     }
-    p.tiles += __shfl_sync(0xffffffffu, ts, 31);
+    p.units += __shfl_sync(0xffffffffu, ts, 31);
     p.items += __shfl_sync(0xffffffffu, is, 31);
     b0 += 32;
     sums(b0, t, it, ts, is);
   }
 }
 
-// The item at `rel` tiles into a request: its KV head and row chunk; `rel`
-// becomes the tile's number in it.
+// The item at `rel` units into a request: its KV head and row chunk; `rel`
+// becomes the tile's number in it (not below nt in the units after its tiles).
 struct ItemAt {
   int h, rch, nt;  // nt: its tiles
 };
@@ -145,13 +151,14 @@ __device__ __forceinline__ ItemAt item_at(const AttnQ8Args& a, const ReqQ8& r, u
   ItemAt x = {0, 0, 0};
   for (;; ++x.h) {
     x.nt = (a.ret_mask >> x.h) & 1ull ? r.tr : r.tl;
-    const uint32_t all = (uint32_t)(x.nt * r.rc);
+    const uint32_t all = (uint32_t)((x.nt + kAqItemCost) * r.rc);
     if (rel < all) break;
     rel -= all;
   }
   if (r.rc > 1) {
-    x.rch = (int)(rel / (uint32_t)x.nt);
-    rel -= (uint32_t)x.rch * (uint32_t)x.nt;
+    const uint32_t each = (uint32_t)(x.nt + kAqItemCost);
+    x.rch = (int)(rel / each);
+    rel -= (uint32_t)x.rch * each;
   }
   return x;
 }
@@ -256,15 +263,20 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
 
   while (at < end) {
     // ---- the segment: tiles [u0, u1) of item (b, h, rch) ----
-    uint32_t rel = at - line.tiles;
-    while (rel >= rq.tiles(R, a.Hkv)) {  // on to the next request that has tiles
-      line.tiles += rq.tiles(R, a.Hkv);
+    uint32_t rel = at - line.units;
+    while (rel >= rq.units(R, a.Hkv)) {  // on to the next request that has tiles
+      line.units += rq.units(R, a.Hkv);
       line.items += (uint32_t)(rq.rc * a.Hkv);
-      rel = at - line.tiles;
+      rel = at - line.units;
       rq = load_req(a, ++b, flags);
     }
     const ItemAt x = item_at(a, rq, rel);
     const int h = x.h, rch = x.rch, nt = x.nt;
+    const uint32_t next = at + (uint32_t)(nt + kAqItemCost) - rel;  // the next item
+    if (rel >= (uint32_t)nt) {
+      at = next;
+      continue;
+    }
     const bool ret = (a.ret_mask >> h) & 1ull;
     const int u0 = (int)rel;
     const int u1 = (int)min((uint32_t)nt, rel + (end - at));
@@ -645,7 +657,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
     }
     fence_async_smem();  // the ring held ordinary stores; the next segment's copies overwrite them
     __syncthreads();
-    at += u1 - u0;
+    at = next;
   }
   if (tid == 0) a.jobs[blockIdx.x] = job;
   if (flags) atomicOr(a.pool.status, flags);
@@ -804,7 +816,7 @@ size_t attn_q8_workspace_bytes(const Shape& sh, int n_tokens, int max_q) {
 bool attn_q8_fits(const Shape& sh, int max_q, int max_seq_len) {
   const int q = small_q(sh, max_q);
   const long long chunks = ((long long)q * sh.G + item_rows(sh, max_q) - 1) / item_rows(sh, max_q);
-  return (double)sh.B * sh.Hkv * (double)chunks * ((max_seq_len - 1) / kAqTile + 1) < 2147483648.0;
+  return (double)sh.B * sh.Hkv * (double)chunks * ((max_seq_len - 1) / kAqTile + 1 + kAqItemCost) < 2147483648.0;
 }
 
 int launch_attn_q8(const Shape& sh, const Q8Pool& pool, const RopeAxes& rope, const AttnQ8Call& c, void* ws,

@@ -79,7 +79,7 @@ int attn_bounds(const Shape& sh, int n_tokens, int max_q, int* max_seq_len) {
   if (*max_seq_len < 0 || *max_seq_len > sh.Lmax) return fail(RTP_ERR_SHAPE, "max_seq_len must be in [0, max_ctx]");
   if (*max_seq_len == 0) *max_seq_len = sh.Lmax;
   if (!attn_q8_fits(sh, max_q, *max_seq_len))
-    return fail(RTP_ERR_SHAPE, "batch * n_kv_heads * query row chunks * ceil(max_seq_len / 32) must stay below 2^31");
+    return fail(RTP_ERR_SHAPE, "batch * n_kv_heads * query row chunks * (ceil(max_seq_len / 32) + 16) must stay below 2^31");
   return RTP_OK;
 }
 

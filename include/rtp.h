@@ -427,7 +427,7 @@ int rtp_append_q8(const rtp_layer_cfg* cfg, const rtp_q8_cache* cache, const voi
 
 /* Host.  Scratch bytes of rtp_attn_q8 for calls of up to n_tokens packed
  * queries, max_q of one request and max_seq_len positions (0: cfg->max_ctx).
- * batch * n_kv_heads * ceil(max_seq_len / 32) * c has to stay below 2^31
+ * batch * n_kv_heads * (ceil(max_seq_len / 32) + 16) * c has to stay below 2^31
  * (RTP_ERR_SHAPE, here and in rtp_attn_q8); c = ceil(max_q G / 8) for fp32
  * layers, at most 2 for bf16 ones. */
 int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_tokens, int max_q,
