@@ -1,11 +1,12 @@
 // C ABI of the layer (include/rtp.h): argument validation, buffer sizes and
 // dispatch to the kernels.  No allocation, no synchronisation, no state beyond
 // a thread-local error message.
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <string>
 
-#include <cmath>
 #include "internal.h"
 
 namespace rtp {
@@ -70,8 +71,10 @@ int make_shape(const rtp_layer_cfg* cfg, Shape* sh) {
   sh->G = G;
   sh->D = cfg->head_dim;
   sh->Lmax = cfg->max_ctx;
-  sh->S = cfg->n_sink;
-  sh->W = cfg->window;
+  // no position lies past max_ctx, so larger ones mean the same; up to 2^23 the
+  // kernels' sums of them (rounded up to tiles, less positions) stay in 32 bits
+  sh->S = std::min(cfg->n_sink, cfg->max_ctx);
+  sh->W = std::min(cfg->window, cfg->max_ctx);
   sh->top_p = cfg->top_p;
   sh->rope_base = cfg->rope_base;
   sh->dtype = cfg->dtype;

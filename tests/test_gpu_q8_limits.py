@@ -1,0 +1,42 @@
+"""The paged 8-bit cache at the ends of what its calls allow: configuration
+values, value and query sizes, batches, rotary axes, streams, lengths that
+fall.  The references and the bounds are those of tests/test_gpu_q8.py unless
+a test gives its own."""
+
+import pytest
+import torch
+
+import head_wise_sparse_local_b200 as rtp
+from test_gpu_q8 import _Attn
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+INT_MAX = 2 ** 31 - 1
+
+
+# ---------------------------------------------------------------------------
+# sinks and windows past every position
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("S,W", [(INT_MAX, 1), (INT_MAX - 30, 5), (INT_MAX - 126, 7), (0, INT_MAX), (3, INT_MAX - 1), (INT_MAX, INT_MAX)])
+def test_every_position_a_sink_or_in_the_window(S, W):
+    a = _Attn([1, 32, 97, 999, 2048], [1, 2, 1, 3, 1], bs=32, S=S, W=W, ret=(1,), seed=41)
+    a.check(a.run())
+    a = _Attn([1500, 40], [300, 1], G=2, bs=32, S=S, W=W, ret=(1,), seed=42)
+    a.check(a.run(), rows={(0, t) for t in range(0, 300, 13)} | {(0, 299), (1, 0)})
+    assert int(a.status) == 0
+
+
+def test_prefill_and_decode_where_every_position_is_a_sink():
+    """The layer's own cache: the same bits as for sinks that just cover the context."""
+    from parity import run_gpu_decode, run_gpu_prefill
+    from synth import LayerShape, make_decode_inputs, make_prefill_inputs
+    outs = []
+    for S in (700, INT_MAX, INT_MAX - 126):
+        sh = LayerShape(batch=1, n_q_heads=8, n_kv_heads=2, head_dim=128, n_sink=S, window=40, top_p=0.85, retrieval=(1,), dtype="bf16")
+        w = dict(seed=31, ctx=260, needles=6, shape=sh)
+        p = run_gpu_prefill(make_prefill_inputs(dict(w, kind="prefill"), T=260, start_pos=0, max_ctx=600))
+        d = run_gpu_decode(make_decode_inputs(dict(w, kind="decode"), max_ctx=600))
+        outs.append((torch.as_tensor(p["out"]), torch.as_tensor(d["out"])))
+    for p, d in outs[1:]:
+        assert torch.equal(p, outs[0][0]) and torch.equal(d, outs[0][1])
