@@ -229,6 +229,8 @@ def _packed(x, cfg, heads: int, name, dev):
     s0, s1, s2 = x.stride()
     if (s2 != 1 or s1 != D) and shape[0] > 0:
         raise ValueError(f"{name}: a token's heads must be dense")
+    if shape[0] > 1 and s0 < heads * D:  # (0, a broadcast, would reach the library as "dense")
+        raise ValueError(f"{name}: tokens must not overlap")
     return x.data_ptr(), s0 if shape[0] > 1 else 0
 
 
