@@ -159,14 +159,21 @@ def rtp_prefill_attn(cfg, cache, q_pre, start_pos, T, w_q, out, sel_bitmask=None
 
 def make_q8_cache(k, v, k_scale, v_scale, status) -> rtp_q8_cache:
     """Describe a pool of blocks: k, v [n_blocks, Hkv, block_size, D] (float8_e4m3fn or
-    uint8), scales [n_blocks, Hkv] fp32, status one int32.  It holds addresses
-    only: keep the tensors alive."""
+    uint8), scales [n_blocks, Hkv] fp32, status one int32, all on one device.  It
+    holds addresses only (keep the tensors alive), and the pool's heads, head_dim
+    and device, which rtp_append_q8 and rtp_attn_q8 hold against the call's."""
     if v.shape != k.shape or k.dim() != 4 or k.element_size() != 1 or v.element_size() != 1:
         raise ValueError("k and v must be [n_blocks, Hkv, block_size, D] of one byte an element")
     if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2] or k_scale.dtype != torch.float32 \
             or v_scale.dtype != torch.float32:
         raise ValueError("k_scale and v_scale must be [n_blocks, Hkv] float32")
-    return rtp_q8_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(status), k.shape[0], k.shape[2])
+    if status.dtype != torch.int32 or status.numel() != 1:
+        raise ValueError("status must be one int32")
+    if any(x.device != k.device for x in (v, k_scale, v_scale, status)):
+        raise ValueError("k, v, k_scale, v_scale and status must be on one device")
+    cache = rtp_q8_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(status), k.shape[0], k.shape[2])
+    cache.made_for = (k.shape[1], k.shape[3], k.get_device())
+    return cache
 
 
 def make_rope(head_dim: int, sections: Sequence[int], interleaved: bool = False) -> rtp_rope_axes:
@@ -234,6 +241,14 @@ def _packed(x, cfg, heads: int, name, dev):
     return x.data_ptr(), s0 if shape[0] > 1 else 0
 
 
+def _check_pool(cache, cfg, dev) -> None:
+    """The call's heads, head_dim and device are the pool's (a description made of bare addresses has none to hold)."""
+    made_for = cache.made_for
+    if made_for is not None and made_for != (cfg.n_kv_heads, cfg.head_dim, dev):
+        raise ValueError(f"the pool has (n_kv_heads, head_dim, CUDA device) {made_for}, the call "
+                         f"{(cfg.n_kv_heads, cfg.head_dim, dev)}")
+
+
 def _device(x, name) -> int:
     """The device of a call's first tensor, which has to be the current one."""
     dev = x.get_device()
@@ -267,6 +282,7 @@ def rtp_page_plan(cfg, block_size, ctx_len, new_len, block_table, free_list, n_f
 
 def rtp_append_q8(cfg, cache, k_pre, v_in, slot_map, pos, rope=None, stream=None) -> None:
     dev, n = _device(k_pre, "k_pre"), k_pre.shape[0]
+    _check_pool(cache, cfg, dev)
     k, ks = _packed(k_pre, cfg, cfg.n_kv_heads, "k_pre", dev)
     v, vs = _packed(v_in, cfg, cfg.n_kv_heads, "v_in", dev)
     if v_in.shape[0] != n:
@@ -291,6 +307,7 @@ def rtp_attn_q8(cfg, cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, 
     if workspace is None:
         raise ValueError("workspace is missing: rtp_attn_q8_workspace_bytes says how much")
     i32, dev, n, B = torch.int32, _device(q_pre, "q_pre"), q_pre.shape[0], cfg.batch
+    _check_pool(cache, cfg, dev)
     q, qs = _packed(q_pre, cfg, cfg.n_q_heads, "q_pre", dev)
     if out.shape != q_pre.shape:
         raise ValueError("out must have q_pre's shape")

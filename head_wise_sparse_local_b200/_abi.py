@@ -54,6 +54,7 @@ class rtp_q8_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("status", ctypes.c_void_p), ("n_blocks", ctypes.c_int),
                 ("block_size", ctypes.c_int)]
+    made_for = None  # (KV heads, head_dim, device) of the tensors it was made from
 
 
 class rtp_rope_axes(ctypes.Structure):

@@ -40,3 +40,23 @@ def test_prefill_and_decode_where_every_position_is_a_sink():
         outs.append((torch.as_tensor(p["out"]), torch.as_tensor(d["out"])))
     for p, d in outs[1:]:
         assert torch.equal(p, outs[0][0]) and torch.equal(d, outs[0][1])
+
+
+# ---------------------------------------------------------------------------
+# a pool that is not the configuration's
+# ---------------------------------------------------------------------------
+def test_a_pool_of_other_heads_is_refused_before_the_call():
+    a = _Attn([100], [1], D=64, hkv=2, G=2, bs=32, seed=3).device()
+    a.call()
+    torch.cuda.synchronize()
+    for kw in (dict(n_kv_heads=4, n_q_heads=8), dict(head_dim=128)):
+        base = dict(batch=1, n_q_heads=4, n_kv_heads=2, head_dim=64, max_ctx=100, n_sink=4, window=100, top_p=1.0, retrieval=(0,))
+        base.update(kw)
+        cfg = rtp.make_cfg(**base)
+        shape = (1, cfg.n_kv_heads, cfg.head_dim)
+        k = torch.zeros(shape, dtype=torch.bfloat16, device=DEV)
+        q = torch.zeros(1, cfg.n_q_heads, cfg.head_dim, dtype=torch.bfloat16, device=DEV)
+        with pytest.raises(ValueError, match="pool"):
+            rtp.rtp_append_q8(cfg, a.cache, k, k, torch.zeros(1, dtype=torch.int64, device=DEV), a.dpos)
+        with pytest.raises(ValueError, match="pool"):
+            rtp.rtp_attn_q8(cfg, a.cache, q, a.dcu, a.dlen, a.dtab, a.dpos, torch.empty_like(q), 1, 0, None, a.ws, a.ws.numel())

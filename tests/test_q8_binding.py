@@ -31,3 +31,43 @@ def test_packed_rows_that_overlap_are_refused():
         assert rtp._packed(torch.zeros(3, heads, 64, dtype=torch.bfloat16), cfg, heads, name, -1)[1] == heads * 64
         wide = torch.zeros(3, 12 * 64, dtype=torch.bfloat16)[:, 128:128 + heads * 64].unflatten(1, (heads, 64))
         assert rtp._packed(wide, cfg, heads, name, -1)[1] == 12 * 64
+
+
+class _FakeCuda:
+    """What make_q8_cache asks of a tensor, on a device of the test's choice."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, index=0):
+        self._x, self.device, self.shape, self.dtype = torch.empty(shape, dtype=dtype), torch.device("cuda", index), torch.Size(shape), dtype
+
+    def __getattr__(self, name):
+        return getattr(self._x, name)
+
+    def get_device(self):
+        return self.device.index
+
+
+def _pool(monkeypatch, heads=2, D=64, status=((1,), torch.int32), devices=(0,) * 5):
+    monkeypatch.setattr(rtp, "_ptr", lambda x: x.data_ptr())
+    dt = torch.uint8
+    return rtp.make_q8_cache(*(_FakeCuda(shape, t, i) for (shape, t), i in zip(
+        (((3, heads, 32, D), dt), ((3, heads, 32, D), dt), ((3, heads), torch.float32), ((3, heads), torch.float32), status), devices)))
+
+
+def test_a_pool_is_held_against_the_call(monkeypatch):
+    cache = _pool(monkeypatch, devices=(1,) * 5)
+    rtp._check_pool(cache, _cfg(), 1)
+    for cfg, dev in ((_cfg(n_kv_heads=4), 1), (_cfg(n_kv_heads=1), 1), (_cfg(head_dim=128), 1), (_cfg(), 0)):
+        with pytest.raises(ValueError, match="pool"):
+            rtp._check_pool(cache, cfg, dev)
+    rtp._check_pool(rtp.rtp_q8_cache(0, 0, 0, 0, 0, 3, 32), _cfg(), 0)  # bare addresses: the caller's word
+
+
+def test_a_pool_of_several_devices_or_of_another_status_is_refused(monkeypatch):
+    _pool(monkeypatch)
+    for k in range(1, 5):
+        with pytest.raises(ValueError, match="device"):
+            _pool(monkeypatch, devices=tuple(int(i == k) for i in range(5)))
+    for status in (((1,), torch.int64), ((2,), torch.int32), ((0,), torch.int32)):
+        with pytest.raises(ValueError, match="status"):
+            _pool(monkeypatch, status=status)
