@@ -322,13 +322,50 @@ def rtp_attn_q8(cfg, cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, 
         _abi.check(rc)
 
 
-class PagedLayer:
+class _Memory:
+    """Torch-allocated memory that is used on whatever streams its owner's calls
+    name.  Torch orders a buffer's former and next users on the stream that was
+    current when it was allocated; the other streams are seen to here."""
+
+    def _settle(self, dev: int) -> None:
+        """What the current stream still does to memory just allocated (its former
+        user's work, its filling) is waited for, so that any stream may use it."""
+        self._dev = dev
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(dev).synchronize()
+
+    def _on(self, stream, tensors) -> int:
+        """The handle of a call's stream; torch is told of streams that it has not
+        seen, so that freed memory waits for them (not of streams made elsewhere,
+        which may be gone by then: synchronise those before the owner goes)."""
+        handle = _raw_stream(stream, self._dev)
+        if handle not in self._streams:
+            self._streams[handle] = None
+            if not isinstance(stream, int):
+                s = torch.cuda.current_stream(self._dev) if stream is None else stream
+                if handle == 0 or s.stream_id != handle:  # (an outside stream's id is its handle)
+                    self._streams[handle] = s
+                    for t in tensors:
+                        t.record_stream(s)
+        return handle
+
+    def _scratch(self, n: int, dev: int) -> torch.Tensor:
+        t = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev))
+        self._settle(dev)
+        for s in self._streams.values():
+            if s is not None:
+                t.record_stream(s)
+        return t
+
+
+class PagedLayer(_Memory):
     """One layer's configuration with a pool of 8-bit blocks and scratch, all
     torch-allocated.  Requests' block tables come from rtp_page_plan and are
     shared by a model's layers; pass the step's to append() and attend().
     attend() calls share one scratch, so they must not overlap each other;
     layers that run side by side, and graphs replayed side by side, take an
-    object each."""
+    object each.  Scratch that has to grow waits for the current stream: where
+    that matters, and before a capture, reserve() the largest call's."""
 
     def __init__(self, shape, max_ctx: int, n_blocks: int, block_size: int = 64, device="cuda", rope=None):
         self.shape = shape
@@ -345,6 +382,8 @@ class PagedLayer:
         self.cache = make_q8_cache(self.k, self.v, self.k_scale, self.v_scale, self.status)
         self.ws = torch.empty(0, dtype=torch.uint8, device=device)
         self._outgrown = []  # scratch that a captured graph or another stream may still use
+        self._streams = {}
+        self._settle(self.k.get_device())
 
     def reserve(self, n_tokens: int, max_q: int, max_seq_len: int = 0) -> None:
         """Scratch for attend() calls of that size; call it before capturing one in a graph."""
@@ -353,15 +392,18 @@ class PagedLayer:
             if self.ws.numel():
                 self._outgrown.append(self.ws)
             # at least twice the last, so that all outgrown ones together are no larger
-            self.ws = torch.empty(max(n, 2 * self.ws.numel()), dtype=torch.uint8, device=self.k.device)
+            self.ws = self._scratch(max(n, 2 * self.ws.numel()), self._dev)
+
+    def _tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale, self.status, self.ws
 
     def append(self, k_pre, v_in, slot_map, pos, stream=None) -> None:
-        rtp_append_q8(self.cfg, self.cache, k_pre, v_in, slot_map, pos, self.rope, stream)
+        rtp_append_q8(self.cfg, self.cache, k_pre, v_in, slot_map, pos, self.rope, self._on(stream, self._tensors()))
 
     def attend(self, q_pre, cu_q, seq_len, block_table, pos, out, max_q: int, max_seq_len: int = 0, stream=None) -> None:
         self.reserve(q_pre.shape[0], max_q, max_seq_len)
         rtp_attn_q8(self.cfg, self.cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, max_seq_len, self.rope,
-                    self.ws, self.ws.numel(), stream)
+                    self.ws, self.ws.numel(), self._on(stream, self._tensors()))
 
     def device_status(self) -> int:
         return int(self.status.item())

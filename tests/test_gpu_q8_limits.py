@@ -60,3 +60,87 @@ def test_a_pool_of_other_heads_is_refused_before_the_call():
             rtp.rtp_append_q8(cfg, a.cache, k, k, torch.zeros(1, dtype=torch.int64, device=DEV), a.dpos)
         with pytest.raises(ValueError, match="pool"):
             rtp.rtp_attn_q8(cfg, a.cache, q, a.dcu, a.dlen, a.dtab, a.dpos, torch.empty_like(q), 1, 0, None, a.ws, a.ws.numel())
+
+
+# ---------------------------------------------------------------------------
+# a layer's own memory on streams that are not the current one
+# ---------------------------------------------------------------------------
+def _layer(n_blocks=60, bs=32, B=2):
+    from synth import LayerShape
+    sh = LayerShape(batch=B, n_q_heads=8, n_kv_heads=2, head_dim=64, n_sink=4, window=100, top_p=1.0, retrieval=(0,), dtype="bf16")
+    return rtp.PagedLayer(sh, 1900, n_blocks, bs)
+
+
+def _busy(stream=None):
+    """About a tenth of a second of work."""
+    with torch.cuda.stream(stream or torch.cuda.current_stream()):
+        torch.cuda._sleep(200_000_000)
+
+
+def test_a_new_layer_can_be_appended_to_on_any_stream():
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    x = torch.randn(4, 2, 64, device=DEV).bfloat16()
+    slots, pos = torch.arange(4, device=DEV), torch.zeros(1, 4, dtype=torch.int32, device=DEV)
+    for busy in (False, True):  # (the first loads the kernels and leaves its blocks to the allocator)
+        torch.cuda.synchronize()
+        if busy:
+            _busy()  # the pool's zeros would wait behind this
+        layer = None
+        layer = _layer()
+        layer.append(x, x, slots, pos, stream=s)
+    torch.cuda.synchronize()
+    assert bool((layer.v[0, :, :4].float() * layer.v_scale[0][:, None, None] != 0).any(-1).all()) and layer.device_status() == 0
+
+
+@pytest.mark.parametrize("how", ["stream argument", "current stream", "raw handle"])
+def test_scratch_is_not_memory_that_another_stream_still_uses(how):
+    a = _Attn([1900, 400], [70, 1], D=64, bs=32, seed=23).device()
+    layer = _layer(a.dk.shape[0])
+    layer.cache = a.cache
+    n = rtp.rtp_attn_q8_workspace_bytes(layer.cfg, 32, a.N, 70)
+    s = torch.cuda.Stream()
+    a.call()  # (loads the kernels)
+    a.out.zero_()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    at = old.data_ptr()
+    torch.cuda.synchronize()
+    _busy()
+    old.fill_(0xFF)
+    pending = torch.cuda.Event()
+    pending.record()
+    del old  # its block is the allocator's to give, and its last user has not run
+    args = (a.dq, a.dcu, a.dlen, a.dtab, a.dpos, a.out, 70)
+    if how == "current stream":
+        with torch.cuda.stream(s):
+            layer.attend(*args)
+    else:
+        layer.attend(*args, stream=s if how == "stream argument" else s.cuda_stream)
+    assert layer.ws.numel() >= n
+    assert pending.query() or not at <= layer.ws.data_ptr() < at + n
+    torch.cuda.synchronize()
+    a.check(a.out.cpu().double(), rows={(0, 0), (0, 33), (0, 69), (1, 0)})
+
+
+def test_memory_of_a_layer_that_goes_waits_for_its_streams():
+    a = _Attn([1900, 400], [70, 1], D=64, bs=32, seed=24).device()
+    s = torch.cuda.Stream()
+    layer = _layer(a.dk.shape[0])
+    layer.cache = a.cache
+    n = rtp.rtp_attn_q8_workspace_bytes(layer.cfg, 32, a.N, 70)
+    layer.reserve(a.N, 70)
+    held = [(t.data_ptr(), t.numel()) for t in (layer.ws, layer.k, layer.v)]
+    torch.cuda.synchronize()
+    _busy(s)
+    layer.attend(a.dq, a.dcu, a.dlen, a.dtab, a.dpos, a.out, 70, stream=s)
+    done = torch.cuda.Event()
+    done.record(s)
+    del layer
+    new = [torch.empty(k, dtype=torch.uint8, device=DEV) for _, k in held]
+    taken = [t.data_ptr() for t in new]
+    assert not done.query()  # (else the test shows nothing)
+    assert not any(at <= p < at + k for p in taken for at, k in held)
+    torch.cuda.synchronize()
+    a.check(a.out.cpu().double(), rows={(0, 0), (0, 33), (0, 69), (1, 0)})
