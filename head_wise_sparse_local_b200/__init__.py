@@ -409,8 +409,10 @@ class PagedLayer(_Memory):
         return int(self.status.item())
 
 
-class Layer:
+class Layer(_Memory):
     """One layer's configuration plus its device cache and scratch (torch-allocated).
+    Calls that share scratch must not overlap; prefill scratch that has to grow
+    waits for the current stream (reserve_prefill() the longest chunk's).
 
     local_cap > 0 selects ring mode: local heads keep only their sinks and a
     ring of local_cap window rows.  k and v are then flat [B, rows, D] buffers
@@ -447,33 +449,44 @@ class Layer:
         self.ws_decode = torch.empty(self.ws_decode_bytes, dtype=torch.uint8, device=device)
         self.ws_prefill = None
         self.ws_prefill_bytes = 0
+        self._outgrown = []  # prefill scratch that a captured graph or another stream may still use
+        self._streams = {}
+        self._settle(self.k.get_device())
         if prefill_T:
             self.reserve_prefill(prefill_T)
 
     def reserve_prefill(self, T: int) -> None:
         n = rtp_prefill_workspace_bytes(self.cfg, T)
         if n > self.ws_prefill_bytes:
+            if self.ws_prefill is not None:
+                self._outgrown.append(self.ws_prefill)
+                # twice the last, up to the GiB that chunks need at most: so outgrown ones stay few
+                n = max(n, min(2 * self.ws_prefill_bytes, 1 << 30))
             self.ws_prefill_bytes = n
-            self.ws_prefill = torch.empty(n, dtype=torch.uint8, device=self.k.device)
+            self.ws_prefill = self._scratch(n, self._dev)
+
+    def _call_stream(self, stream) -> int:
+        t = (self.k, self.v, self.kidx_full, self.status, self.ws_decode)
+        return self._on(stream, t if self.ws_prefill is None else t + (self.ws_prefill,))
 
     def append(self, k_pre, v_in, start_pos, w_k, stream=None) -> None:
-        rtp_append_kv(self.cfg, self.cache, k_pre, v_in, start_pos, k_pre.shape[1], w_k, stream)
+        rtp_append_kv(self.cfg, self.cache, k_pre, v_in, start_pos, k_pre.shape[1], w_k, self._call_stream(stream))
 
     def decode(self, q_pre, seq_len, w_q, out, max_seq_len: int = 0, sel_bitmask=None,
                sel_count=None, stream=None) -> None:
         rtp_decode_attn(self.cfg, self.cache, q_pre, seq_len, max_seq_len, w_q, out, sel_bitmask,
-                        sel_count, self.ws_decode, self.ws_decode_bytes, stream)
+                        sel_count, self.ws_decode, self.ws_decode_bytes, self._call_stream(stream))
 
     def recall(self, q_pre, seq_len, sel_bitmask, recall, max_seq_len: int = 0, stream=None) -> None:
         rtp_decode_recall(self.cfg, self.cache, q_pre, seq_len, max_seq_len, sel_bitmask, recall,
-                          self.ws_decode, self.ws_decode_bytes, stream)
+                          self.ws_decode, self.ws_decode_bytes, self._call_stream(stream))
 
     def prefill(self, q_pre, start_pos, w_q, out, sel_bitmask=None, sel_tau=None, sel_jcut=None,
                 sel_count=None, stream=None) -> None:
         T = q_pre.shape[1]
         self.reserve_prefill(T)
         rtp_prefill_attn(self.cfg, self.cache, q_pre, start_pos, T, w_q, out, sel_bitmask, sel_tau,
-                         sel_jcut, sel_count, self.ws_prefill, self.ws_prefill_bytes, stream)
+                         sel_jcut, sel_count, self.ws_prefill, self.ws_prefill_bytes, self._call_stream(stream))
 
     def device_status(self) -> int:
         return int(self.status.item())

@@ -144,3 +144,55 @@ def test_memory_of_a_layer_that_goes_waits_for_its_streams():
     assert not any(at <= p < at + k for p in taken for at, k in held)
     torch.cuda.synchronize()
     a.check(a.out.cpu().double(), rows={(0, 0), (0, 33), (0, 69), (1, 0)})
+
+
+def test_prefill_scratch_on_another_stream_and_in_a_graph_that_outlives_it():
+    """The layer's own cache: a chunk on a stream that is not the current one, then a
+    longer one; the first one's graph still has its scratch."""
+    from synth import LayerShape
+    sh = LayerShape(batch=1, n_q_heads=8, n_kv_heads=2, head_dim=64, n_sink=4, window=40, top_p=0.9, retrieval=(1,), dtype="bf16")
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    x = [torch.randn(1, 900, h, 64, device=DEV, generator=gen).bfloat16() for h in (8, 2, 2)]
+    w_q, w_k = torch.randn(1, 16, 64, device=DEV, generator=gen), torch.randn(1, 16, 64, device=DEV, generator=gen)
+    start, s = torch.zeros(1, dtype=torch.int32, device=DEV), torch.cuda.Stream()
+
+    def chunk(layer, T, out, stream=None):
+        layer.append(x[1][:, :T].contiguous(), x[2][:, :T].contiguous(), start, w_k, stream=stream)
+        layer.prefill(x[0][:, :T].contiguous(), start, w_q, out, stream=stream)
+
+    out = {T: torch.empty(1, T, 8, 64, dtype=torch.bfloat16, device=DEV) for T in (300, 900)}
+    layer = rtp.Layer(sh, 1024)
+    for T in out:
+        chunk(layer, T, out[T])
+    want = {T: o.clone() for T, o in out.items()}
+    layer = rtp.Layer(sh, 1024)
+    n = rtp.rtp_prefill_workspace_bytes(layer.cfg, 300)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    at = old.data_ptr()
+    q, k, v = (y[:, :300].contiguous() for y in x)
+    torch.cuda.synchronize()
+    _busy()
+    old.fill_(0xFF)
+    pending = torch.cuda.Event()
+    pending.record()
+    del old
+    layer.append(k, v, start, w_k, stream=s)
+    layer.prefill(q, start, w_q, out[300].zero_(), stream=s)
+    assert pending.query() or not at <= layer.ws_prefill.data_ptr() < at + n
+    torch.cuda.synchronize()
+    layer.prefill(q, start, w_q, out[300], stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out[300], want[300])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            layer.prefill(q, start, w_q, out[300])
+    small = layer.ws_prefill
+    chunk(layer, 900, out[900])
+    assert torch.equal(out[900], want[900]) and layer.ws_prefill is not small and any(t is small for t in layer._outgrown)
+    out[300].zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[300], want[300]) and layer.device_status() == 0
