@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
 
     // ---- the stream ----
     float o[KS][NR][4];
-    float M[NR], l[NR];
+    float M[NR], l[NR], lv_low = -CUDART_INF_F;  // lv_low: kAqFar below log2 of the largest value scale that M may hold
 #pragma unroll
     for (int m = 0; m < KS; ++m)
 #pragma unroll
@@ -501,12 +501,13 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
         move = move || mx[r] > M[r] + kAqRescale || (M[r] == -CUDART_INF_F && mx[r] > M[r]);
       }
       if (__any_sync(0xffffffffu, move)) {
+        lv_low = fmaxf(lv_low, fmaxf(lv[0], lv[1]) - kAqFar);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float mn = fmaxf(M[r], mx[r]);
           const float f = M[r] == -CUDART_INF_F ? 0.f : ex2(M[r] - mn);
+          l[r] = M[r] == -CUDART_INF_F ? 0.f : lower(l[r], M[r] - mn);
           M[r] = mn;
-          l[r] *= f;
           // O^T's columns are rows 2 t4 and 2 t4 + 1 of the row group
           const float f0 = __shfl_sync(0xffffffffu, f, 8 * t4), f1 = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
 #pragma unroll
@@ -518,8 +519,16 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
           }
         }
       }
+      float rv[2] = {ex2(kAqSumLift - lv[0]), ex2(kAqSumLift - lv[1])};
+      if (fminf(lv[0], lv[1]) < lv_low) {  // (the warp agrees) the tile's share of l from the logits without the scales
+        rv[0] = rv[1] = 0.f;
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            l[r] += ex2(x[r][e] - lv[e >> 2] + (kAqLift + kAqSumLift - (M[r] == -CUDART_INF_F ? 0.f : M[r])));
+      }
       uint32_t wh[2][NR][2], wl[2][NR][2];  // [16 positions][row group][b0, b1]
-      const float rv[2] = {ex2(-lv[0]), ex2(-lv[1])};
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float sub = kAqLift - (M[r] == -CUDART_INF_F ? 0.f : M[r]);
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
         os.y = fmaf(v.y, f, os.y);
         os.z = fmaf(v.z, f, os.z);
         os.w = fmaf(v.w, f, os.w);
-        ls = fmaf(p[w * kW + D + 1], f, ls);
+        ls += lower(p[w * kW + D + 1], p[w * kW + D] - ms);
       }
       if (alone) {
         write_out(r, d, os, ls);
@@ -694,9 +703,8 @@ __global__ void __launch_bounds__(kAqJoinWarps * 32) attn_q8_join_kernel(const _
   float l = 0.f;
   for (int p = tid; p < job.np; p += kAqJoinWarps * 32) {
     const float2 y = *reinterpret_cast<const float2*>(ml + (size_t)p * a.rows * 2);
-    const float f = ex2(y.x - ms);
-    s_f[p] = f;
-    l = fmaf(y.y, f, l);
+    s_f[p] = ex2(y.x - ms);
+    l += lower(y.y, y.x - ms);
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);

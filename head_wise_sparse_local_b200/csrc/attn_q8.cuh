@@ -10,6 +10,16 @@ namespace rtp {
 
 constexpr float kAqRescale = 8.f;  // the running maximum moves when a tile exceeds it by 2^8
 constexpr float kAqLift = 6.f;     // weights are held 2^6 up (at most 2^14 in fp16), away from fp16's small end
+// Value scales lie up to 2^185 apart.  A weight that vanishes beside another's scale,
+// 2^(x - M) = 0, may still have its share of l, w / vs: where a tile's scales lie more
+// than 2^64 below the largest that M may hold, the tile adds to l from the logits
+// without the scales.  (Nearer ones lose less than 2^-44 of l: M is at most the largest
+// logit plus log2 of that scale, so a weight that vanishes is below 2^-67 of the largest.)
+// l is held 2^24 up besides, which keeps its ends, 2^-115 for the largest scale and
+// 2^101 for 2^23 positions of the least, away from fp32's.
+constexpr float kAqFar = 64.f;
+constexpr float kAqSumLift = 24.f;
+constexpr float kAqSumUnit = 16777216.f;  // 2^24
 
 // 256 query rows of one (request, KV head): row r is token (row0 + r) / G of
 // the request, at position i0 + that, and query head (row0 + r) % G of the
@@ -92,15 +102,21 @@ __device__ __forceinline__ float ex2(float x) {
   return e;
 }
 
+// l 2^d, d <= 0, in two steps: 2^d alone may vanish where the product does not.
+__device__ __forceinline__ float lower(float l, float d) {
+  const float e = fmaxf(d, -120.f);
+  return l * ex2(e) * ex2(d - e);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// out = O / l of one row element.
+// out = O / l of one row element (l held 2^24 up).
 template <typename T>
 __device__ __forceinline__ T finish(float o, float l) {
-  return from_f32<T>(l == 0.f ? 0.f : o / l);  // l = 0: no position of the row is there
+  return from_f32<T>(l == 0.f ? 0.f : o * kAqSumUnit / l);  // l = 0: no position of the row is there
 }
 
 // The chunk kernel (bf16 layers): workspace, and its launches for the requests

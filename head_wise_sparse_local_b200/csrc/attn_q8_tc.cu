@@ -87,8 +87,10 @@ struct CSmem {
 
 // Scales of 16 positions of a tile, and which 32-position words are there.
 struct __align__(16) CMeta {
-  float4 g[8];  // k scale, log2(v scale), 1 / v scale; g[0].w: 1 where all are there
+  // k scale, log2(v scale), 2^24 / v scale (0 where `far`, and for blocks that are not there); g[0].w: 1 where all are there and not `far`
+  float4 g[8];
   uint32_t there[4];
+  int far;  // the value scales so far, of the item's tiles in this CTA, lie more than kAqFar apart
 };
 
 // First position of an item's u-th tile.
@@ -295,7 +297,9 @@ __device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {  //
       : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
 
-// (x, y) = (2^x, 2^y) on the FMA pipe, the cubic of ex2_poly on a pair.
+// (x, y) = (2^x, 2^y) on the FMA pipe, the cubic of ex2_poly on a pair.  Below -125, masked
+// positions among them, 2^-125: 0 in fp16, and in l 2^(24 - 125) / vs, in all under 2^-44 of it
+// beside scales up to 2^64 larger; where they lie farther apart l is not formed from these.
 __device__ __forceinline__ void ex2_poly2(float& x, float& y) {
   const float a = fmaxf(x, -125.f), b = fmaxf(y, -125.f);
   asm("{\n\t.reg .b64 v, t, f, p, c;\n\t.reg .b32 t0, t1, p0, p1;\n\t"
@@ -378,6 +382,50 @@ struct CWalk {
   }
 };
 
+// A row's maximum and l after a tile whose value scales lie far below the largest: its share of l
+// comes from the logits without the scales, against the tile's own maximum, to which O and l are
+// brought first.  Seldom called, so it is kept out of the softmax's loop.
+template <int D>
+__device__ __forceinline__ float2 far_tile(const CMeta& m, uint32_t tSs, uint32_t tOs, bool has_o, float rs, float M, float l) {
+  float mx = M;
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    uint32_t s[16];
+    tmem_ld16(tSs + 16 * q, s);
+    tmem_wait_ld();
+    const float4 g = m.g[q];
+    float t = -CUDART_INF_F;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) t = fmaxf(t, __uint_as_float(s[e]));
+    mx = fmaxf(mx, fmaf(t, rs * g.x, g.y));
+  }
+  const float f = M == -CUDART_INF_F ? 0.f : ex2(M - mx);
+  l = M == -CUDART_INF_F ? 0.f : lower(l, M - mx);
+  if (has_o) {
+#pragma unroll 1
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t o[16];
+      tmem_ld16(tOs + k * 16, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+      tmem_st16(tOs + k * 16, o);
+    }
+    tmem_wait_st();
+  }
+  const float sub = kAqLift + kAqSumLift - (mx == -CUDART_INF_F ? 0.f : mx);
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    uint32_t s[16];
+    tmem_ld16(tSs + 16 * q, s);
+    tmem_wait_ld();
+    const float fq = rs * m.g[q].x;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) l += ex2(fmaf(__uint_as_float(s[e]), fq, sub));
+  }
+  return make_float2(mx, l);
+}
+
 struct CBars {
   uint64_t raw_full[2], raw_empty[2];                       // K's rows as stored, and V's
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];    // by stage
@@ -386,9 +434,11 @@ struct CBars {
 };
 
 // Asks for the rows of the CTA's tile T, whose blocks the lanes hold in `id`, and writes its scales.
+// `span`: log2 of the least and the largest value scale so far of the item's tiles in this CTA.
 template <int D>
 __device__ __forceinline__ bool load_rows_of_tile(const AttnQ8Args& a, const CWalk& w, int T, int id, CBars& bars,
-                                                  unsigned char* raw, CMeta* meta, volatile int* s_abort, uint32_t (&asked)[2]) {
+                                                  unsigned char* raw, CMeta* meta, volatile int* s_abort, uint32_t (&asked)[2],
+                                                  float2& span) {
   const int lane = threadIdx.x & 31;
   const int per = kCKeys >> a.pool.log_bs, box = 1 << a.pool.log_bs;  // copies a tile, of so many rows
   float ks = 0.f, vs = 0.f;
@@ -399,11 +449,24 @@ __device__ __forceinline__ bool load_rows_of_tile(const AttnQ8Args& a, const CWa
   // copy p < per covers the blocks of lanes p * 8 / per ..; a block that is not there: any rows, they become zeros
   const int mine = __shfl_sync(0xffffffffu, id, (lane & 7) * (8 / per) & 7);
   const int y = (((mine < 0 ? 0 : mine) * a.Hkv + w.c.h) << a.pool.log_bs);  // (a tile starts on a block)
-  if (!c_wait(&bars.raw_empty[0], ((uint32_t)T & 1u) ^ 1u, a, s_abort)) return false;
-  CMeta& m = meta[T & 7];
   const unsigned there = __ballot_sync(0xffffffffu, lane < 8 && id >= 0);
   vs = fmaxf(vs, kQ8ScaleMin);
-  if (lane < 8) m.g[lane] = make_float4(fmaxf(ks, kQ8ScaleMin), __log2f(vs), 1.f / vs, there == 0xffu ? 1.f : 0.f);
+  const float lv = __log2f(vs);
+  if (id >= 0) {
+    span.x = fminf(span.x, lv);
+    span.y = fmaxf(span.y, lv);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {  // (lanes 8 and up repeat the first ones)
+    span.x = fminf(span.x, __shfl_xor_sync(0xffffffffu, span.x, o));
+    span.y = fmaxf(span.y, __shfl_xor_sync(0xffffffffu, span.y, o));
+  }
+  const bool far = span.x < span.y - kAqFar;
+  const float4 g = make_float4(fmaxf(ks, kQ8ScaleMin), lv, id < 0 || far ? 0.f : kAqSumUnit / vs, there == 0xffu && !far ? 1.f : 0.f);
+  if (!c_wait(&bars.raw_empty[0], ((uint32_t)T & 1u) ^ 1u, a, s_abort)) return false;
+  CMeta& m = meta[T & 7];
+  if (lane < 8) m.g[lane] = g;
+  if (lane == 0) m.far = far;
   if (lane < 4)
     m.there[lane] = ((there >> (2 * lane) & 1u) ? 0xffffu : 0u) | ((there >> (2 * lane + 1) & 1u) ? 0xffff0000u : 0u);
   __syncwarp();
@@ -511,6 +574,11 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
             tmem_st32(tSs + x * 32, v);
           }
           tmem_wait_st();
+          if (m.far) {  // (the slot agrees)
+            const float2 y = far_tile<D>(m, tSs, tOs, i > 0, rs, M, l);
+            M = y.x;
+            l = y.y;
+          }
         }
         // ---- the weights against the running maximum, 64 columns at a time (one rolled loop:
         // the instruction cache feeds it), their fp16 over columns already read ----
@@ -602,10 +670,11 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
       if (!ok || !c_wait(&bars.o_full[slot], seg & 1u, a, &s_abort)) { ok = false; break; }
       tc_fence_after();
       if (poison) l = CUDART_NAN_F;
+      else if (M == -CUDART_INF_F) l = 0.f;  // the row sees nothing (ex2_poly2 gives masked positions 2^-125, not 0)
       const bool alone = w.u0 == 0 && w.nt == c.tiles;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D;
       const size_t pn = (size_t)(2 * blockIdx.x + (w.u0 > 0 ? 0 : 1));  // the partial: four dims of all rows lie together
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : kAqSumUnit / l;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {
         float o[32];
@@ -787,6 +856,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
       int T = 0, flags = 0;
       bool ok = true;
       for (bool more = w.start(a); more && ok; more = w.next(a)) {
+        float2 span = make_float2(CUDART_INF_F, -CUDART_INF_F);
         for (int i = 0; i < w.nt && ok; ++i, ++T) {
           // lane g < 8: the block of positions [16 g, 16 g + 16) of the tile; -1: there is none
           int id = -1;
@@ -798,7 +868,7 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
               id = -1;
             }
           }
-          ok = load_rows_of_tile<D>(a, w, T, id, bars, dsm + SM::kOffRaw, s_meta, &s_abort, nr);
+          ok = load_rows_of_tile<D>(a, w, T, id, bars, dsm + SM::kOffRaw, s_meta, &s_abort, nr, span);
           if (i > 0) continue;
           for (int slot = 0; slot < (w.two ? 2 : 1) && ok; ++slot) {
             if (!(ok = c_wait(&bars.q_empty[slot], (nq[slot] & 1u) ^ 1u, a, &s_abort))) break;
@@ -867,7 +937,7 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
 #pragma unroll
     for (int j = 0; j < J; ++j) p[j] = *reinterpret_cast<const float4*>(a.cpart + ((part(k) * (D / 4) + d4 + j) * kCGroup + r) * 4);
     const float f = ex2(ml.x - ms);
-    l = fmaf(ml.y, f, l);
+    l += lower(ml.y, ml.x - ms);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       o[j].x = fmaf(p[j].x, f, o[j].x);
@@ -877,7 +947,7 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
     }
   }
   const int tok = c.q0 + ((c.row0 + r) >> a.log_g), hq = c.h * a.G + ((c.row0 + r) & (a.G - 1));
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : kAqSumUnit / l;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)tok * a.Hq + hq) * D + d4 * 4;
 #pragma unroll
   for (int j = 0; j < J; j += 2) {

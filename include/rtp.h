@@ -442,7 +442,8 @@ int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_
  *   out = softmax(RoPE(q, pos) . k_j / sqrt(D)) v_j    k_j, v_j as stored, times their scales
  * One token a request (decode), a few, or chunks, in any mix.  Arithmetic is
  * on tensor cores with fp32 accumulation; queries (scaled by a power of two a
- * row) and softmax weights enter them as fp16.  Queries enter as two fp16
+ * row) and softmax weights enter them as fp16
+ * (scales of any size may lie beside one another).  Queries enter as two fp16
  * parts (22 bits) where max_q * G <= 8, and for fp32 layers, whose weights do
  * so too.  Blocks may be shared between requests.  v holds no NaN at cached
  * positions (rtp_append_q8 writes none): a weight of 0 does not hide one.

@@ -196,3 +196,62 @@ def test_prefill_scratch_on_another_stream_and_in_a_graph_that_outlives_it():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[300], want[300]) and layer.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# value scales of any size beside one another
+# ---------------------------------------------------------------------------
+def _with_value_scales(a, exps, b=0):
+    """Request b's blocks get these value scales, the least one together with zero values."""
+    for i, e in enumerate(exps):
+        blk = a.table[b, i]
+        a.pool.vs[blk] = 2.0 ** e
+        if e == -64:
+            a.pool.v[blk] = 0.0
+    return a
+
+
+FAR_APART = [(-64, 100, -64, -40, 110, -64, 3, -64), (110, -64, -64, -64, -64, -64, -64, 105), (-64,) * 7 + (112,), (112,) + (-64,) * 7,
+             (60, -64, 56, -63, -64, 0, 61, -64)]
+
+
+@pytest.mark.parametrize("exps", FAR_APART)
+@pytest.mark.parametrize("dtype,G,new", [("fp32", 4, 1), ("bf16", 8, 1), ("bf16", 4, 4), ("bf16", 4, 60)])
+@pytest.mark.parametrize("ret", [(0,), ()])
+def test_value_scales_over_their_whole_range(exps, dtype, G, new, ret):
+    """Every position has about the same weight, so a block whose weights vanish
+    beside another's scale would take its share of the sum with it."""
+    a = _Attn([512], [new], bs=64, hkv=1, G=G, ret=ret, S=20, W=200, dtype=dtype, seed=11, q_scale=0.2)
+    a.check(_with_value_scales(a, exps).run())
+
+
+def test_value_scales_over_their_whole_range_in_cut_items():
+    """Partials of CTAs, and of warps, whose maxima lie as far apart."""
+    exps = [(-64, 110, -64, -64, 40, -64, -64, 105, 0)[i % 9] for i in range(313)]
+    a = _Attn([20000], [1], bs=64, hkv=2, G=4, ret=(0, 1), S=0, W=1, seed=12, q_scale=0.2)
+    a.check(_with_value_scales(a, exps).run())
+    a = _Attn([20000], [70], bs=64, hkv=2, G=4, ret=(0, 1), S=0, W=1, seed=13, q_scale=0.2)
+    a.check(_with_value_scales(a, sorted(exps)).run(), rows={(0, t) for t in range(0, 70, 23)})
+    a = _Attn([20000], [70], bs=64, hkv=2, G=4, ret=(0, 1), S=0, W=1, seed=13, q_scale=0.2)
+    a.check(_with_value_scales(a, sorted(exps, reverse=True)).run(), rows={(0, t) for t in range(0, 70, 23)})
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_a_query_that_sees_nothing_gets_zero_whatever_lies_behind_it(new):
+    """A chunk's first queries see only blocks that are not there; the positions
+    after theirs have values of any scale."""
+    for e in (-64, -20, 0, 10, 40, 100):
+        a = _Attn([128], [new], bs=16, hkv=1, G=4, ret=(0,), seed=17)
+        _with_value_scales(a, (e,) * 8)
+        a.device()
+        tab = a.dtab.clone()
+        tab[0, :3] = -1
+        if new == 1:
+            tab[0, :] = -1
+        a.dtab.copy_(tab)
+        a.call()
+        torch.cuda.synchronize()
+        got = a.out.cpu().double()
+        assert bool((got[:20] == 0).all()), e  # positions 28 to 47 (or 127 alone)
+        if new > 1:
+            a.check(got, rows={(0, t) for t in range(20, 100, 9)}, there=[torch.arange(128) >= 48])
