@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
       float m = 0.f;
       for (int k = lane; k < D; k += 32) m = fmaxf(m, fabsf(s_q[r * SM::kQPitch + k]));
       m = warp_max(m);
-      if (lane == 0) s_qs[r] = query_scale(m);
+      if (lane == 0) s_qs[r] = query_scale<-118>(m);
     }
     __syncthreads();
     uint32_t qa[KS][4];

@@ -89,10 +89,13 @@ __device__ __forceinline__ ReqRows load_rows(const AttnQ8Args& a, int b, int& fl
 }
 
 // Factor 2^e that brings a query row's largest magnitude m into [2^8, 2^9), so
-// that neither fp16's largest value nor its smallest step is in the way.
+// that neither fp16's largest value nor its smallest step is in the way; not below
+// 2^least, which rows of m < 2^(least + 8) are left under.  At -118 the factor's
+// reciprocal is still a normal number.
+template <int least>
 __device__ __forceinline__ float query_scale(float m) {
   int e = (int)(__float_as_uint(m) >> 23) - 127 - 8;
-  e = m == 0.f ? 0 : min(max(e, -40), 110);
+  e = m == 0.f ? 0 : min(max(e, least), 119);
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 

@@ -72,7 +72,9 @@ constexpr int kCCtas = 148;               // one an SM of a B200
 constexpr int kCItemCost = 3;             // units of the line after an item's tiles: its start and end cost about as much
 constexpr int kCMinShare = 4;             // units a CTA takes at least
 constexpr int kCTmemCols = 512;
-constexpr float kCRescale = 9.f;          // the running maximum moves past 2^9: weights reach 2^15, below fp16's largest
+// The running maximum moves past 2^9: weights reach 2^15, and 2^15.5 where M is rounded by a half
+// (from 2^24, scores of 2^23), below fp16's largest.
+constexpr float kCRescale = 9.f;
 
 template <int D>
 struct CSmem {
@@ -195,7 +197,8 @@ __global__ void __launch_bounds__(kCPrep) chunk_prep_kernel(const __grid_constan
         x1[h][i] = y1;
         m = fmaxf(m, fmaxf(fabsf(y1), fabsf(x2[h][i])));
       }
-      const float sc = query_scale(warp_max(m)), inv = 1.f / sc;
+      // (times the least key scale, 2^-64, and log2(e) / sqrt(D) the factor stays above 0: it multiplies the -inf of masked positions)
+      const float sc = query_scale<-59>(warp_max(m)), inv = 1.f / sc;
       const size_t row = (size_t)t * a.Hq + h0 + h;
       __half* o = a.cq + row * D + lane * PP;
       Halves y1, y2;

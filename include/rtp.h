@@ -443,9 +443,10 @@ int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_
  * One token a request (decode), a few, or chunks, in any mix.  Arithmetic is
  * on tensor cores with fp32 accumulation; queries (scaled by a power of two a
  * row) and softmax weights enter them as fp16
- * (scales of any size may lie beside one another).  Queries enter as two fp16
- * parts (22 bits) where max_q * G <= 8, and for fp32 layers, whose weights do
- * so too.  Blocks may be shared between requests.  v holds no NaN at cached
+ * (value scales of any size may lie beside one another; requests of more than
+ * 32 query rows (n G) a KV head, in bf16, lose bits of query rows below 2^-64, and
+ * want scores q . k / sqrt(D) of less than 2^23: larger ones may answer NaN).  Queries enter as two fp16 parts (22 bits)
+ * where max_q * G <= 8, and for fp32 layers, whose weights do so too.  Blocks may be shared between requests.  v holds no NaN at cached
  * positions (rtp_append_q8 writes none): a weight of 0 does not hide one.
  *
  *   q_pre        [n_tokens][Hq][D] dtype, device, pre-RoPE; rows q_stride

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import head_wise_sparse_local_b200 as rtp
+import q8_reference as ref
 from test_gpu_q8 import _Attn
 
 pytestmark = pytest.mark.gpu
@@ -255,3 +256,67 @@ def test_a_query_that_sees_nothing_gets_zero_whatever_lies_behind_it(new):
         assert bool((got[:20] == 0).all()), e  # positions 28 to 47 (or 127 alone)
         if new > 1:
             a.check(got, rows={(0, t) for t in range(20, 100, 9)}, there=[torch.arange(128) >= 48])
+
+
+# ---------------------------------------------------------------------------
+# queries of any size
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,G,new", [("fp32", 4, 1), ("bf16", 8, 1), ("bf16", 4, 4), ("bf16", 4, 60)])
+@pytest.mark.parametrize("size", [-100, -70, -45, 50])
+def test_small_and_large_queries_against_keys_of_the_inverse_size(dtype, G, new, size):
+    if new == 60:
+        size = max(size, -64)  # chunks
+    a = _Attn([300], [new], bs=32, hkv=1, G=G, ret=(0,), dtype=dtype, seed=19, q_scale=1.5 * 2.0 ** size)
+    a.pool.ks *= 2.0 ** -size
+    a.check(a.run())
+
+
+@pytest.mark.parametrize("dtype,new", [("fp32", 1), ("fp32", 60), ("bf16", 1), ("bf16", 4)])  # (chunks want scores below 2^23)
+def test_the_largest_finite_queries(dtype, new):
+    """Scores of 2^60 and more: the position of the largest takes all, where it leads
+    the next by more than the scores' error."""
+    a = _Attn([200], [new], bs=32, hkv=1, G=4, ret=(0,), dtype=dtype, seed=20, q_scale=1.0)
+    a.q = (a.q / a.q.float().abs().amax() * 2.0 ** 127).to(a.dt)
+    a.pos.zero_()  # not turned: a rotation could pass the largest number
+    a.pool.ks[:] = ref.SCALE_MIN
+    got, led = a.run(), 0
+    assert bool(torch.isfinite(got).all())
+    k, v = a.pool.rows(a.table[0], 200, 0)
+    for t in range(new):
+        for g in range(4):
+            q = a.q[t, g].double()
+            s = (k @ q)[:200 - new + t + 1]
+            err = float((k.abs() @ q.abs()).max()) * (a.r_q() + 2.0 ** -20)
+            top = torch.topk(s, 2)
+            if float(top.values[0] - top.values[1]) > 4 * err:
+                led += 1
+                want = v[top.indices[0]]
+                assert bool(((got[t, g] - want).abs() <= want.abs() * 2.0 ** -8).all())
+    assert led >= 2 * new
+
+
+@pytest.mark.parametrize("ascending", [False, True])
+def test_chunk_scores_up_to_2_23(ascending):
+    """Scores that grow (or fall) by powers of two over the context, to just below
+    2^23: one position takes all."""
+    a = _Attn([400], [60], bs=32, hkv=1, G=4, ret=(0,), seed=21, q_scale=1.0)
+    a.pos.zero_()
+    for i in range(13):  # 13 blocks of 32
+        a.pool.ks[a.table[0, i]] = 2.0 ** ((i if ascending else 12 - i) + 1)
+    qm = float((a.q.double().abs().sum(-1)).amax()) * 448 * 2.0 ** 13 / 128 ** 0.5
+    a.q = (a.q.double() * (2.0 ** 22 * 1.9 / qm)).to(a.dt)
+    got = a.run()
+    assert bool(torch.isfinite(got).all()) and int(a.status) == 0
+    k, v = a.pool.rows(a.table[0], 400, 0)
+    led = 0
+    for t in range(0, 60, 7):
+        for g in range(4):
+            q = a.q[t, g].double()
+            s = (k @ q)[:400 - 60 + t + 1] / 128 ** 0.5
+            err = float((k.abs() @ q.abs()).max()) / 128 ** 0.5 * (a.r_q() + 2.0 ** -20)
+            top = torch.topk(s, 2)
+            if float(top.values[0] - top.values[1]) > 4 * err + 40:
+                led += 1
+                want = v[top.indices[0]]
+                assert bool(((got[t, g] - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -10)).all())
+    assert led >= 12
