@@ -3,12 +3,14 @@ values, value and query sizes, batches, rotary axes, streams, lengths that
 fall.  The references and the bounds are those of tests/test_gpu_q8.py unless
 a test gives its own."""
 
+import math
+
 import pytest
 import torch
 
 import head_wise_sparse_local_b200 as rtp
 import q8_reference as ref
-from test_gpu_q8 import _Attn
+from test_gpu_q8 import AXIS3, _Attn
 
 pytestmark = pytest.mark.gpu
 
@@ -320,3 +322,97 @@ def test_chunk_scores_up_to_2_23(ascending):
                 want = v[top.indices[0]]
                 assert bool(((got[t, g] - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -10)).all())
     assert led >= 12
+
+
+# ---------------------------------------------------------------------------
+# bf16 layers held to what their own roundings allow
+# ---------------------------------------------------------------------------
+class _Strict(_Attn):
+    """With one fp16 part a row's queries (over 8 query rows a KV head), the bound of
+    test_gpu_q8.py takes the rounding of every query dim at its worst, and leaves large
+    scores nearly free.  Here the reference rounds the queries as the kernels do, so
+    what is left of the score's error is
+      - dims that the fp32 rotation (off by 1.125 2^-22 (|x1| + |x2|)) may bring to
+        either side of a rounding border: a step of fp16 times |k|;
+      - one truncation, 2^-23 of sum |q k|, for each 16 products, D / 16 <= 8 of them;
+      - the factor from products to base 2 (three roundings and a reciprocal root) and
+        the scaled score's own rounding: 2^-20 of the score, and 2^-18.
+    A weight p_j is then off by b_j = expm1 of that, and in chunks by the cubic's 7.5e-5;
+    the numerator's weights also by their fp16 rounding 2^-11, or 2^-25 where they are
+    subnormal, against a largest weight of 2^5 or more.  So
+      |out - o| <= sum p_j b_j |v_j - o| + 2^-11 sum p_j |v_j| + L 2^-30 448 max_j p_j vs_j
+                   + (L / 16 + 64) 2^-23 sum p_j |v_j| + |o| 2^-8
+    (times 1 + 2 max b for the second order)."""
+
+    def strict(self, got, rows):
+        told = []  # rows of which the bound rejects an answer of zeros
+        sc = 1.0 / math.sqrt(self.D)
+        th = ref.angles(self.pos, self.axis, self.D)
+        qr, x = ref.rotate(self.q.double(), th), self.q.double().abs()
+        h = self.D // 2
+        pair = x[..., :h] + x[..., h:]
+        off = torch.cat([pair, pair], -1) * 1.25 * 2.0 ** -22
+        chunk = self.max_q * self.G > 32
+        for b in range(self.B):
+            L, n = self.lens[b], self.new[b]
+            own = chunk and (n * self.G > 32 or self.B == 1)  # its kernel
+            for hk in range(self.hkv):
+                k, v = self.pool.rows(self.table[b], L, hk)
+                vs = self.pool.vs[torch.as_tensor(self.table[b][:-(-L // self.bs)]), hk].repeat_interleave(self.bs)[:L]
+                for t in range(n):
+                    if (b, t) not in rows:
+                        continue
+                    seen = ref.visible(L - n + t, L, hk in self.ret, self.S, self.W)
+                    ks, vv, vss = k[seen], v[seen], vs[seen]
+                    for g in range(self.G):
+                        tok, hq = self.cu[b] + t, hk * self.G + g
+                        y, d = qr[tok, hq], off[tok, hq]
+                        unit = 2.0 ** (math.floor(math.log2(float(y.abs().max()))) - 8)
+                        q = (y / unit).half().double() * unit
+                        step = (((y + d) / unit).half().double() - ((y - d) / unit).half().double()).abs() * unit
+                        s = ks @ q * sc
+                        e = (ks.abs() @ step + ks.abs() @ q.abs() * 2.0 ** -20) * sc + s.abs() * 2.0 ** -20 + 2.0 ** -18
+                        p = torch.softmax(s, 0)
+                        o = p @ vv
+                        bj = torch.expm1(e) + (7.5e-5 if own else 0.0)
+                        A = p @ vv.abs()
+                        bound = (((p * bj) @ (vv - o).abs()) * (1 + 2 * float((bj * p).sum())) + A * (2.0 ** -11 + (L / 16 + 64) * 2.0 ** -23)
+                                 + L * 2.0 ** -30 * 448 * float((p * vss).max()) + o.abs() * 2.0 ** -8)
+                        err = (got[tok, hq] - o).abs()
+                        assert bool((err <= bound).all()), (b, t, hq, float((err / bound).max()))
+                        told.append(bool((o.abs() > 2 * bound).any()))
+        assert sum(told) >= 0.95 * len(told), (sum(told), len(told))
+
+
+@pytest.mark.parametrize("q_scale", [0.3, 1.5, 6.0, 20.0])
+@pytest.mark.parametrize("new,G", [(60, 4), (4, 4), (300, 1)])
+def test_large_scores_and_value_scales_far_apart(q_scale, new, G):
+    a = _Strict([512], [new], bs=64, hkv=1, G=G, ret=(0,), seed=35, q_scale=q_scale)
+    for i, e in enumerate((-30, -20, 0, 10, -7, -5, -60, -1)):
+        a.pool.vs[a.table[0, i]] = 2.0 ** e
+    a.pool.v[a.table[0, 3]] = 0.0
+    a.pool.vs[a.table[0, 3]] = ref.SCALE_MIN
+    a.strict(a.run(), {(0, t) for t in range(0, new, max(1, new // 15))})
+
+
+@pytest.mark.parametrize("q_scale", [1.5, 12.0])
+@pytest.mark.parametrize("new", [[600, 64, 3], [17, 200, 9]])
+def test_chunks_drafts_and_windows_strictly(q_scale, new):
+    a = _Strict([1500, 700, 333], new, D=128, hkv=2, G=2, bs=32, S=33, W=150, ret=(1,), sections=AXIS3[128], seed=36, q_scale=q_scale)
+    a.strict(a.run(), {(b, t) for b, n in enumerate(new) for t in range(0, n, max(1, n // 9))})
+
+
+@pytest.mark.parametrize("q_scale", [1.5, 12.0])
+def test_cut_items_strictly(q_scale):
+    for lens, new, D in (([20000], [70], 128), ([15000, 9000], [100, 5], 64)):
+        a = _Strict(lens, new, D=D, hkv=2, G=4, bs=64, S=64, W=2048, ret=(1,), seed=37, q_scale=q_scale)
+        a.strict(a.run(), {(b, t) for b, n in enumerate(new) for t in (0, n // 2, n - 1)})
+
+
+def test_scores_that_rise_along_the_context():
+    """The maximum moves again and again, in either half of a tile: what was weighed
+    before it is brought down by factors that are exact."""
+    a = _Strict([1024], [100], bs=16, hkv=1, G=4, ret=(0,), seed=38, q_scale=6.0)
+    for i in range(64):
+        a.pool.ks[a.table[0, i]] = 2.0 ** -9 if i % 3 else 2.0 ** (-9 + i // 11)
+    a.strict(a.run(), {(0, t) for t in range(0, 100, 9)})
