@@ -21,8 +21,8 @@
 //                    thread a row: 64 columns of S at a time are read from TMEM
 //                    and their fp16 weights against the running maximum written
 //                    over columns already read; where they exceed the maximum by
-//                    2^9, it moves, and O and the tile's weights so far are
-//                    rescaled.  One rolled loop: the same in straight-line code
+//                    2^9, it moves, up to a whole number, and O and the tile's weights
+//                    so far are rescaled by the exact power of two.  One rolled loop: the same in straight-line code
 //                    for 4 x 32 columns took 475 us for the 418 (the instruction
 //                    cache could not feed it), a rolled loop over 32 columns 409
 //                    for 384, whole rows in registers and S read twice more still;
@@ -402,6 +402,7 @@ __device__ __forceinline__ float2 far_tile(const CMeta& m, uint32_t tSs, uint32_
     for (int e = 0; e < 16; ++e) t = fmaxf(t, __uint_as_float(s[e]));
     mx = fmaxf(mx, fmaf(t, rs * g.x, g.y));
   }
+  mx = ceilf(mx);
   const float f = M == -CUDART_INF_F ? 0.f : ex2(M - mx);
   l = M == -CUDART_INF_F ? 0.f : lower(l, M - mx);
   if (has_o) {
@@ -609,7 +610,8 @@ __global__ void __launch_bounds__(kCThreads, 1) attn_q8_chunk_kernel(const __gri
           const bool need = mx > M + kCRescale || (M == -CUDART_INF_F && mx > M);
           if (__any_sync(0xffffffffu, need)) {
             // rare after an item's first columns: the maximum moves, and with it O, l and the
-            // tile's weights so far
+            // tile's weights so far (by whole powers of two: in fp16 too the factor is exact)
+            mx = ceilf(mx);
             const float f = need ? (M == -CUDART_INF_F ? 0.f : ex2f(M - mx)) : 1.f;
             M = need ? mx : M;
             l *= f;
