@@ -377,6 +377,10 @@ int rtp_q8_cache_bytes(const rtp_layer_cfg* cfg, int n_blocks, int block_size, s
  * (RTP_DEV_BLOCKS), ctx_len[b] + new_len[b] > max_ctx or
  * its packed tokens pass max_tokens (RTP_DEV_POSITION).  ctx_len[b] outside [0, max_ctx]
  * counts as 0 cached and no new tokens (RTP_DEV_SEQ_LEN).
+ * rtp_attn_q8 knows nothing of refusals: a refused request keeps its rows in cu_new,
+ * so its outputs there are made as if its newest cached tokens were the new ones, and
+ * mean nothing.  Where *status has one of these bits, its rows are those with slot -1
+ * ahead of cu_new[B]; the caller drops them, or plans the step again without it.
  *
  *   ctx_len, new_len  [B] int32, device
  *   block_table       [B][ceil(max_ctx / block_size)] int32, device, in/out

@@ -416,3 +416,66 @@ def test_scores_that_rise_along_the_context():
     for i in range(64):
         a.pool.ks[a.table[0, i]] = 2.0 ** -9 if i % 3 else 2.0 ** (-9 + i // 11)
     a.strict(a.run(), {(0, t) for t in range(0, 100, 9)})
+
+
+# ---------------------------------------------------------------------------
+# steps of a serving loop
+# ---------------------------------------------------------------------------
+class _Serving:
+    """A layer with the arrays of a loop, and what it ought to hold."""
+
+    def __init__(self, B, n_blocks, bs=16, max_ctx=256, cap=256, D=64, hkv=2, G=4, seed=51):
+        from synth import LayerShape
+        sh = LayerShape(batch=B, n_q_heads=hkv * G, n_kv_heads=hkv, head_dim=D, n_sink=4, window=60, top_p=1.0, retrieval=(1,), dtype="bf16")
+        self.layer, self.B, self.bs, self.cap, self.D = rtp.PagedLayer(sh, max_ctx, n_blocks, bs), B, bs, cap, D
+        self.a = _Attn([1] * B, [1] * B, D=D, hkv=hkv, G=G, bs=bs, S=4, W=60, ret=(1,))
+        self.a.pool, self.gen = ref.Pool(n_blocks, hkv, bs, D), torch.Generator().manual_seed(seed)
+        i32 = dict(dtype=torch.int32, device=DEV)
+        self.table, self.free = torch.full((B, -(-max_ctx // bs)), -1, **i32), torch.arange(n_blocks, **i32)
+        self.n_free, self.length, self.cu = torch.tensor([n_blocks], **i32), torch.zeros(B, **i32), torch.zeros(B + 1, **i32)
+        self.slots, self.pos = torch.zeros(cap, dtype=torch.int64, device=DEV), torch.zeros(cap, **i32)
+
+    def plan(self, new):
+        rtp.rtp_page_plan(self.layer.cfg, self.bs, self.length, torch.tensor(new, dtype=torch.int32, device=DEV), self.table, self.free,
+                          self.n_free, self.length, self.cu, self.slots, self.pos, self.n_free, self.layer.status)
+
+    def step(self, new, refused=()):
+        """Plan, append, attend; the outputs of the requests that are served are checked."""
+        a, cap = self.a, self.cap
+        self.plan(new)
+        k, v = (torch.randn(cap, a.hkv, self.D, generator=self.gen).bfloat16() for _ in range(2))
+        q = torch.randn(cap, a.hkv * a.G, self.D, generator=self.gen).bfloat16()
+        out = torch.full((cap, a.hkv * a.G, self.D), 77.0, dtype=torch.bfloat16, device=DEV)
+        self.layer.append(k.to(DEV), v.to(DEV), self.slots, self.pos)
+        mq = max(max(new), 1)
+        self.layer.attend(q.to(DEV), self.cu, self.length, self.table, self.pos, out, mq)
+        torch.cuda.synchronize()
+        p = self.pos.cpu()[None]
+        a.pool.append(ref.rotate(k.double(), ref.angles(p, a.axis, self.D)), v, self.slots.cpu())
+        a.lens, a.new = [int(x) for x in self.length], [max(x, 0) for x in new]
+        a.cu, a.table, a.q, a.pos, a.max_q = self.cu.cpu().numpy(), self.table.cpu().numpy(), q, p, mq
+        a.check(out.cpu().double(), rows={(b, t) for b in range(self.B) if b not in refused for t in range(a.new[b])})
+        assert bool((out[sum(a.new):] == 77.0).all())
+        return out
+
+
+def test_a_refused_request_beside_others():
+    """Out of blocks: the request's rows are those without a slot, nothing of it is
+    stored, the others' outputs are right, and it is served once there is room."""
+    s = _Serving(3, 8)
+    s.step([40, 30, 16])  # 3, 2 and 1 blocks of 8
+    held = (s.layer.k.clone().view(torch.uint8), s.table.clone())
+    s.step([8, 40, 0], refused=(1,))  # the second wants 3 more
+    # (attention says too that 30 cached positions cannot hold 40 queries)
+    assert s.layer.device_status() == rtp.RTP_DEV_BLOCKS | rtp.RTP_DEV_SEQ_LEN
+    slots, cu = s.slots.cpu(), s.cu.tolist()
+    assert s.length.tolist() == [48, 30, 16] and int(s.n_free) == 2 and cu == [0, 8, 48, 48]
+    assert bool((slots[8:48] == -1).all()) and bool((slots[:8] >= 0).all())
+    own = s.table[1, :2].long()
+    assert torch.equal(s.layer.k.view(torch.uint8)[own], held[0][own]) and torch.equal(s.table[1], held[1][1])
+    s.layer.status.zero_()
+    s.step([1, 20, -1])  # a block from the third
+    assert s.layer.device_status() == 0 and s.length.tolist() == [49, 50, 0] and int(s.n_free) == 0
+    s.step([1, 17, 0], refused=(1,))  # here its newest 17 cached tokens answer in place of the new ones
+    assert s.layer.device_status() == rtp.RTP_DEV_BLOCKS and s.length.tolist() == [50, 50, 0]
+    assert s.slots[:19].lt(0).tolist() == [False] + [True] * 18
