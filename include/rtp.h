@@ -371,6 +371,13 @@ int rtp_q8_cache_bytes(const rtp_layer_cfg* cfg, int n_blocks, int block_size, s
  * `top` is n_free plus the blocks of ended requests.  Requests must not share
  * blocks.
  *
+ * A request's length may fall between steps (a draft's tokens were rejected).  The plan
+ * knows its blocks by ctx_len alone: where ceil(length / block_size) falls too, table
+ * entries from there on are no longer its own and would be lost.  The caller gives them
+ * back before the next plan, by one in which they are a request of their own that ends:
+ * batch rows of a table that begin with those entries, ctx_len[b] = block_size times
+ * their number, new_len[b] = -1, max_tokens = 0.
+ *
  * A request that cannot be served is refused: it takes no block, seq_len[b] =
  * ctx_len[b], its tokens get slot -1 (so rtp_append_q8 skips them), the others
  * are served as if it were there.  That is where before[b] + need > top

@@ -479,3 +479,34 @@ def test_a_refused_request_beside_others():
     s.step([1, 17, 0], refused=(1,))  # here its newest 17 cached tokens answer in place of the new ones
     assert s.layer.device_status() == rtp.RTP_DEV_BLOCKS and s.length.tolist() == [50, 50, 0]
     assert s.slots[:19].lt(0).tolist() == [False] + [True] * 18
+
+
+def test_lengths_that_fall_and_blocks_that_go_back():
+    """Drafts of which some tokens are rejected: within a block, over one edge and over
+    several; every block stays either a request's or free."""
+    s = _Serving(3, 30, seed=52)
+    bs, cols = s.bs, s.table.shape[1]
+
+    def accounted():
+        held = [int(x) for b in range(3) for x in s.table[b, :-(-int(s.length[b]) // bs)]]
+        return sorted(held + s.free[:int(s.n_free)].tolist()) == list(range(30))
+
+    def fall(to):
+        """The lengths after verification; blocks behind them go back."""
+        had, s.length = s.length, torch.tensor(to, dtype=torch.int32, device=DEV)
+        keep, had = (s.length + bs - 1) // bs, (had + bs - 1) // bs
+        at = (keep[:, None] + torch.arange(cols, device=DEV)).clamp_max(cols - 1)
+        none = torch.empty(0, dtype=torch.int32, device=DEV)
+        scratch = torch.empty(3, dtype=torch.int32, device=DEV)
+        rtp.rtp_page_plan(s.layer.cfg, bs, ((had - keep) * bs).int(), torch.full_like(scratch, -1), s.table.gather(1, at.long()).contiguous(),
+                          s.free, s.n_free, scratch, torch.empty(4, dtype=torch.int32, device=DEV), none.long(), none, s.n_free, s.layer.status)
+
+    s.step([30, 16, 47])
+    for new, to in (([8, 8, 8], [33, 17, 48]), ([20, 40, 1], [33, 18, 49]), ([70, 15, 20], [35, 33, 49]), ([1, 1, 1], [36, 34, 50]),
+                    ([16, 16, 16], [36, 34, 50]), ([13, 15, 15], [49, 49, 65])):
+        s.step(new)
+        assert accounted()
+        fall(to)
+        assert accounted()
+    s.step([1, -1, 1])
+    assert accounted() and s.layer.device_status() == 0
