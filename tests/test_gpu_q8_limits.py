@@ -10,7 +10,7 @@ import torch
 
 import head_wise_sparse_local_b200 as rtp
 import q8_reference as ref
-from test_gpu_q8 import AXIS3, _Attn
+from test_gpu_q8 import AXIS3, _Attn, _Held
 
 pytestmark = pytest.mark.gpu
 
@@ -510,3 +510,89 @@ def test_lengths_that_fall_and_blocks_that_go_back():
         assert accounted()
     s.step([1, -1, 1])
     assert accounted() and s.layer.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# rotary axes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("D,sections,interleaved", [(64, (20, 12), False), (128, (10, 20, 30, 4), False), (64, (8, 12, 12), True),
+                                                    (128, (16, 16, 16, 16), True), (128, (0, 64), False), (128, (1, 62, 1), True)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_two_to_four_axes_in_turn_or_dealt_out(D, sections, interleaved, dtype):
+    rope = rtp.make_rope(D, sections, interleaved)
+    axis = list(rope.axis[:D // 2])
+    assert [axis.count(k) for k in range(len(sections))] == list(sections)
+    gen = torch.Generator().manual_seed(D + len(sections))
+    h = _Held(12, 2, 16, D, dtype, sections=sections)
+    h.rope, h.axis = rope, axis
+    for n, first in ((70, 3), (4, 73)):  # a chunk, a step
+        h.append(torch.randn(n, 2, D, generator=gen).to(h.dt), torch.randn(n, 2, D, generator=gen).to(h.dt),
+                 torch.arange(first, first + n), h.positions(n, gen))
+        h.check()
+    for new in ([1, 1], [3, 2], [60, 1]):
+        a = _Attn([300, 90], new, D=D, hkv=2, G=4, bs=32, dtype=dtype, sections=sections, seed=61)
+        a.rope, a.axis = rope, axis
+        a.check(a.run(), rows={(0, 0), (0, new[0] - 1), (0, new[0] // 2), (1, 0)})
+
+
+# ---------------------------------------------------------------------------
+# batches
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B,every", [(300, 7), (700, 31)])
+def test_chunks_in_batches_of_more_than_256(B, every):
+    """Idle, decoding and drafting requests, and chunks among them on both sides of 256."""
+    new = [(0, 1, 1, 3, 1)[b % 5] if b % every else 9 + b % 40 for b in range(B)]
+    lens = [n + (b * 37) % 150 + (n == 0) for b, n in enumerate(new)]
+    a = _Attn(lens, new, D=64, hkv=2, G=4, bs=16, S=3, W=40, ret=(1,), seed=62, pad=11)
+    got = a.run()
+    some = {(b, t) for b, n in enumerate(new) if b % every == 0 or b % 17 == 0 or b > B - 4 for t in {0, n // 2, n - 1} if n}
+    a.check(got, rows=some)
+    assert bool((got[sum(new):] == 77.0).all()) and int(a.status) == 0
+
+
+def test_a_batch_of_4096():
+    """The largest that a plan takes: a token each, and the same with one chunk."""
+    B = 4096
+    for chunk in (0, 80):
+        new = [1] * B
+        new[3000] = max(1, chunk)
+        lens = [n + b % 33 for b, n in enumerate(new)]
+        a = _Attn(lens, new, D=64, hkv=1, G=2, bs=16, S=2, W=9, ret=(0,), seed=63)
+        a.check(a.run(), rows={(b, 0) for b in range(0, B, 61)} | {(3000, t) for t in range(0, new[3000], 9)} | {(B - 1, 0)})
+        assert int(a.status) == 0
+
+
+@pytest.mark.parametrize("G,max_q", [(1, 40), (4, 200), (8, 7)])
+def test_one_token_where_many_are_allowed(G, max_q):
+    """Alone, and in rows of its own behind nothing: n_tokens below a chunk's tile of rows."""
+    for lens, new in (([500], [1]), ([500, 33], [1, 0]), ([500], [2])):
+        a = _Attn(lens, new, G=G, hkv=2, bs=32, seed=64)
+        a.max_q = max_q
+        a.check(a.run())
+        assert int(a.status) == 0
+
+
+def test_two_calls_at_once_and_in_graphs():
+    """Two layers' calls of every kind, on two streams and replayed side by side: the
+    bits of each alone."""
+    made = []
+    for seed, new in ((65, [1, 2, 1]), (66, [90, 1, 5])):
+        a = _Attn([3000, 700, 90], new, bs=32, seed=seed).device()
+        a.call()
+        torch.cuda.synchronize()
+        made.append((a, a.out.clone(), torch.cuda.Stream(), torch.cuda.CUDAGraph()))
+        with torch.cuda.stream(made[-1][2]):
+            with torch.cuda.graph(made[-1][3], stream=made[-1][2]):
+                a.call()
+    for how in ("calls", "graphs"):
+        for a, _, _, _ in made:
+            a.out.zero_()
+            a.ws.fill_(0xA5)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for a, _, s, g in made:
+                with torch.cuda.stream(s):
+                    g.replay() if how == "graphs" else a.call()
+        torch.cuda.synchronize()
+        for a, want, _, _ in made:
+            assert torch.equal(a.out, want), how
