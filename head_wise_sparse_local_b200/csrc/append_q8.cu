@@ -114,13 +114,6 @@ struct AppPart {
   Four<T> k1, k2, v1, v2;
 };
 
-// The largest of three numbers; a NaN wins.
-__device__ __forceinline__ float max3_nan(float x, float y, float z) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
-  return m;
-}
-
 // The largest number >= 0 of the warp.
 __device__ __forceinline__ float warp_max_positive(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));

@@ -40,6 +40,7 @@
 // 21 us (70 MB); 8 requests of 8K to 32K positions 24 us (95 MB), as drafts 39 us
 // (16 rows a chunk, so their tiles are read twice).
 #include "attn_q8.cuh"
+#include "tc.cuh"
 #include "tensor_map.h"
 
 namespace rtp {
@@ -161,14 +162,6 @@ __device__ __forceinline__ ItemAt item_at(const AttnQ8Args& a, const ReqQ8& r, u
     rel -= (uint32_t)x.rch * each;
   }
   return x;
-}
-
-__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* tm, int y, uint64_t* bar, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;"
-      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(0), "r"(y), "l"(pol)
-      : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -320,10 +313,10 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
       }
       cp_async_arrive_noinc(&bar[s]);
       mbar_expect_tx(&bar[s], (uint32_t)SM::kStage);
-      tma_tile(dst, &a.tm_k, y[0], &bar[s], pol);
-      if (split) tma_tile(dst + 16 * D, &a.tm_k, y[1], &bar[s], pol);
-      tma_tile(dst + kAqTile * D, &a.tm_v, y[0], &bar[s], pol);
-      if (split) tma_tile(dst + kAqTile * D + 16 * D, &a.tm_v, y[1], &bar[s], pol);
+      tma_load_2d(dst, &a.tm_k, 0, y[0], &bar[s], pol);
+      if (split) tma_load_2d(dst + 16 * D, &a.tm_k, 0, y[1], &bar[s], pol);
+      tma_load_2d(dst + kAqTile * D, &a.tm_v, 0, y[0], &bar[s], pol);
+      if (split) tma_load_2d(dst + kAqTile * D + 16 * D, &a.tm_v, 0, y[1], &bar[s], pol);
     };
     // ---- queries: asked for before the stream's copies, which fill the memory system for
     // microseconds; a thread turns a rotary pair of all the chunk's rows of one token ----
@@ -505,7 +498,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float mn = fmaxf(M[r], mx[r]);
-          const float f = M[r] == -CUDART_INF_F ? 0.f : ex2(M[r] - mn);
+          const float f = M[r] == -CUDART_INF_F ? 0.f : ex2f(M[r] - mn);
           l[r] = M[r] == -CUDART_INF_F ? 0.f : lower(l[r], M[r] - mn);
           M[r] = mn;
           // O^T's columns are rows 2 t4 and 2 t4 + 1 of the row group
@@ -519,14 +512,14 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
           }
         }
       }
-      float rv[2] = {ex2(kAqSumLift - lv[0]), ex2(kAqSumLift - lv[1])};
+      float rv[2] = {ex2f(kAqSumLift - lv[0]), ex2f(kAqSumLift - lv[1])};
       if (fminf(lv[0], lv[1]) < lv_low) {  // (the warp agrees) the tile's share of l from the logits without the scales
         rv[0] = rv[1] = 0.f;
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            l[r] += ex2(x[r][e] - lv[e >> 2] + (kAqLift + kAqSumLift - (M[r] == -CUDART_INF_F ? 0.f : M[r])));
+            l[r] += ex2f(x[r][e] - lv[e >> 2] + (kAqLift + kAqSumLift - (M[r] == -CUDART_INF_F ? 0.f : M[r])));
       }
       uint32_t wh[2][NR][2], wl[2][NR][2];  // [16 positions][row group][b0, b1]
 #pragma unroll
@@ -536,7 +529,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
         for (int q = 0; q < 2; ++q) {
           float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(x[r][4 * q + e] + sub);
+          for (int e = 0; e < 4; ++e) w[e] = ex2f(x[r][4 * q + e] + sub);
           l[r] = fmaf((w[0] + w[1]) + (w[2] + w[3]), rv[q], l[r]);
           wh[q][r][0] = pack_f16(w[0], w[1]);
           wh[q][r][1] = pack_f16(w[2], w[3]);
@@ -641,7 +634,7 @@ __global__ void __launch_bounds__(kAqThreads, kAqCtasPerSm) attn_q8_kernel(const
       float ls = 0.f;
 #pragma unroll
       for (int w = 0; w < kAqWarps; ++w) {
-        const float f = ex2(p[w * kW + D] - ms);
+        const float f = ex2f(p[w * kW + D] - ms);
         const float4 v = *reinterpret_cast<const float4*>(p + w * kW + d);
         os.x = fmaf(v.x, f, os.x);
         os.y = fmaf(v.y, f, os.y);
@@ -703,7 +696,7 @@ __global__ void __launch_bounds__(kAqJoinWarps * 32) attn_q8_join_kernel(const _
   float l = 0.f;
   for (int p = tid; p < job.np; p += kAqJoinWarps * 32) {
     const float2 y = *reinterpret_cast<const float2*>(ml + (size_t)p * a.rows * 2);
-    s_f[p] = ex2(y.x - ms);
+    s_f[p] = ex2f(y.x - ms);
     l += lower(y.y, y.x - ms);
   }
 #pragma unroll

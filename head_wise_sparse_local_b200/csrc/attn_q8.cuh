@@ -99,16 +99,10 @@ __device__ __forceinline__ float query_scale(float m) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-  return e;
-}
-
 // l 2^d, d <= 0, in two steps: 2^d alone may vanish where the product does not.
 __device__ __forceinline__ float lower(float l, float d) {
   const float e = fmaxf(d, -120.f);
-  return l * ex2(e) * ex2(d - e);
+  return l * ex2f(e) * ex2f(d - e);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -284,11 +284,6 @@ __device__ __forceinline__ int find_item(const long long* prefix, int n, long lo
   return lo;
 }
 
-__device__ __forceinline__ float max3_nan(float x, float y, float z) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
-  return m;
-}
 __device__ __forceinline__ float max_nan(float x, float y) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
@@ -403,7 +398,7 @@ __device__ __forceinline__ float2 far_tile(const CMeta& m, uint32_t tSs, uint32_
     mx = fmaxf(mx, fmaf(t, rs * g.x, g.y));
   }
   mx = ceilf(mx);
-  const float f = M == -CUDART_INF_F ? 0.f : ex2(M - mx);
+  const float f = M == -CUDART_INF_F ? 0.f : ex2f(M - mx);
   l = M == -CUDART_INF_F ? 0.f : lower(l, M - mx);
   if (has_o) {
 #pragma unroll 1
@@ -425,7 +420,7 @@ __device__ __forceinline__ float2 far_tile(const CMeta& m, uint32_t tSs, uint32_
     tmem_wait_ld();
     const float fq = rs * m.g[q].x;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) l += ex2(fmaf(__uint_as_float(s[e]), fq, sub));
+    for (int e = 0; e < 16; ++e) l += ex2f(fmaf(__uint_as_float(s[e]), fq, sub));
   }
   return make_float2(mx, l);
 }
@@ -941,7 +936,7 @@ __global__ void __launch_bounds__(256) attn_q8_chunk_join_kernel(const __grid_co
     float4 p[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) p[j] = *reinterpret_cast<const float4*>(a.cpart + ((part(k) * (D / 4) + d4 + j) * kCGroup + r) * 4);
-    const float f = ex2(ml.x - ms);
+    const float f = ex2f(ml.x - ms);
     l += lower(ml.y, ml.x - ms);
 #pragma unroll
     for (int j = 0; j < J; ++j) {

@@ -125,6 +125,13 @@ __device__ __forceinline__ unsigned long long mass36(float s, float m) {
   return __float2ull_rn(mass_x36(s, m));
 }
 
+// 2^x by the hardware approximation (relative error about 2^-22; -inf -> +0).
+__device__ __forceinline__ float ex2f(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
+}
+
 // ---------------------------------------------------------------------------
 // reductions
 // ---------------------------------------------------------------------------

@@ -23,6 +23,13 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// The largest of three numbers; a NaN wins.
+__device__ __forceinline__ float max3_nan(float x, float y, float z) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+
 // Least power of two s >= 2^-64 with a <= 448 s, for finite a >= 0.  448 is
 // 1.75 * 2^8: with a = m 2^e, s is 2^(e-8) where m <= 1.75 and 2^(e-7) above.
 __device__ __forceinline__ float q8_scale(float a) {

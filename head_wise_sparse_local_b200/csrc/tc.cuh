@@ -181,13 +181,6 @@ __device__ __forceinline__ float max3f(float x, float y, float z) {
   return m;
 }
 
-// 2^x by the hardware approximation (relative error about 2^-22; -inf -> +0).
-__device__ __forceinline__ float ex2f(float x) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-  return e;
-}
-
 // Packed fp32 pairs (one instruction for two lanes of arithmetic).
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {  // (x, y) += (a, b)
   asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
