@@ -259,6 +259,11 @@ def _device(x, name) -> int:
     return dev
 
 
+def _table_cols(cfg, block_size) -> int:
+    """Entries of a block table's row (none for a block size that the library refuses)."""
+    return -(-cfg.max_ctx // block_size) if block_size > 0 else 0
+
+
 def _raw_stream(stream, dev) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -268,7 +273,7 @@ def _raw_stream(stream, dev) -> int:
 def rtp_page_plan(cfg, block_size, ctx_len, new_len, block_table, free_list, n_free, seq_len, cu_new,
                   slot_map, positions, n_free_out, status, stream=None) -> None:
     i32, dev, B = torch.int32, _device(ctx_len, "ctx_len"), cfg.batch
-    cols = -(-cfg.max_ctx // block_size) if block_size > 0 else 0
+    cols = _table_cols(cfg, block_size)
     n = slot_map.numel()
     rc = _lib.rtp_page_plan(cfg, block_size, _arg(ctx_len, i32, "ctx_len", dev, B), _arg(new_len, i32, "new_len", dev, B),
                             _arg(block_table, i32, "block_table", dev, B * cols), _arg(free_list, i32, "free_list", dev),
@@ -314,7 +319,7 @@ def rtp_attn_q8(cfg, cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, 
     if workspace.numel() < workspace_bytes:
         raise ValueError("workspace_bytes is more than the workspace has")
     rc = _lib.rtp_attn_q8(cfg, cache, q, qs, _arg(cu_q, i32, "cu_q", dev, B + 1), _arg(seq_len, i32, "seq_len", dev, B),
-                          _arg(block_table, i32, "block_table", dev, B * -(-cfg.max_ctx // cache.block_size)),
+                          _arg(block_table, i32, "block_table", dev, B * _table_cols(cfg, cache.block_size)),
                           _arg(pos, i32, "pos", dev, n * (rope.n_axes if rope is not None else 1)), rope, n, max_q,
                           max_seq_len, _arg(out, q_pre.dtype, "out", dev), _arg(workspace, torch.uint8, "workspace", dev),
                           workspace_bytes, _raw_stream(stream, dev))

@@ -596,3 +596,21 @@ def test_two_calls_at_once_and_in_graphs():
         torch.cuda.synchronize()
         for a, want, _, _ in made:
             assert torch.equal(a.out, want), how
+
+
+@pytest.mark.parametrize("B,G", [(1, 4), (3, 8)])
+def test_calls_in_which_no_request_has_a_query(B, G):
+    """Rows behind the last stay as they were, with chunks allowed and without."""
+    a = _Attn([50] * B, [0] * B, G=G, hkv=2, bs=16, seed=67, pad=5)
+    for max_q in (1, 3, 40):
+        a.max_q = max_q
+        assert bool((a.run() == 77.0).all()) and int(a.status) == 0
+
+
+def test_a_bare_description_of_no_block_size_is_refused():
+    a = _Attn([50], [1], seed=68).device()
+    cache = rtp.rtp_q8_cache(a.dk.data_ptr(), a.dv.data_ptr(), a.dks.data_ptr(), a.dvs.data_ptr(), a.status.data_ptr(), a.dk.shape[0], 0)
+    with pytest.raises((ValueError, rtp.RtpError)):
+        rtp.rtp_attn_q8(a.cfg, cache, a.dq, a.dcu, a.dlen, a.dtab, a.dpos, a.out, 1, 0, None, a.ws, a.ws.numel())
+    with pytest.raises(rtp.RtpError):
+        rtp.rtp_append_q8(a.cfg, cache, a.dq[:, :2].contiguous(), a.dq[:, :2].contiguous(), torch.zeros(1, dtype=torch.int64, device=DEV), a.dpos)

@@ -71,3 +71,7 @@ def test_a_pool_of_several_devices_or_of_another_status_is_refused(monkeypatch):
     for status in (((1,), torch.int64), ((2,), torch.int32), ((0,), torch.int32)):
         with pytest.raises(ValueError, match="status"):
             _pool(monkeypatch, status=status)
+
+
+def test_table_rows_of_block_sizes_that_are_refused():
+    assert [rtp._table_cols(_cfg(max_ctx=100), bs) for bs in (16, 128, 0, -64)] == [7, 1, 0, 0]
