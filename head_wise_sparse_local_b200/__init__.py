@@ -224,10 +224,8 @@ def _refuse(x, dtype, name, dev, n) -> None:
     raise ValueError(f"{name} must have {n} elements")
 
 
-def _packed(x, cfg, heads: int, name, dev):
-    """(address, elements between tokens) of packed [N, heads, D] rows, dense or a slice of wider rows."""
-    D = cfg.head_dim
-    dt = torch.bfloat16 if cfg.dtype == RTP_BF16 else torch.float32
+def _packed(x, D: int, dt, heads: int, name, dev):
+    """(address, elements between tokens) of packed [N, heads, D] rows of dt, dense or a slice of wider rows."""
     shape = x.shape
     if x.dtype is not dt or len(shape) != 3 or shape[1] != heads or shape[2] != D:
         raise ValueError(f"{name} must be a CUDA [N, {heads}, {D}] tensor of {dt}")
@@ -241,12 +239,10 @@ def _packed(x, cfg, heads: int, name, dev):
     return x.data_ptr(), s0 if shape[0] > 1 else 0
 
 
-def _check_pool(cache, cfg, dev) -> None:
+def _check_pool(cache, heads: int, D: int, dev) -> None:
     """The call's heads, head_dim and device are the pool's (a description made of bare addresses has none to hold)."""
-    made_for = cache.made_for
-    if made_for is not None and made_for != (cfg.n_kv_heads, cfg.head_dim, dev):
-        raise ValueError(f"the pool has (n_kv_heads, head_dim, CUDA device) {made_for}, the call "
-                         f"{(cfg.n_kv_heads, cfg.head_dim, dev)}")
+    if cache.made_for is not None and cache.made_for != (heads, D, dev):
+        raise ValueError(f"the pool has (n_kv_heads, head_dim, CUDA device) {cache.made_for}, the call {(heads, D, dev)}")
 
 
 def _device(x, name) -> int:
@@ -287,9 +283,10 @@ def rtp_page_plan(cfg, block_size, ctx_len, new_len, block_table, free_list, n_f
 
 def rtp_append_q8(cfg, cache, k_pre, v_in, slot_map, pos, rope=None, stream=None) -> None:
     dev, n = _device(k_pre, "k_pre"), k_pre.shape[0]
-    _check_pool(cache, cfg, dev)
-    k, ks = _packed(k_pre, cfg, cfg.n_kv_heads, "k_pre", dev)
-    v, vs = _packed(v_in, cfg, cfg.n_kv_heads, "v_in", dev)
+    heads, D, dt = cfg.n_kv_heads, cfg.head_dim, torch.bfloat16 if cfg.dtype == RTP_BF16 else torch.float32
+    _check_pool(cache, heads, D, dev)
+    k, ks = _packed(k_pre, D, dt, heads, "k_pre", dev)
+    v, vs = _packed(v_in, D, dt, heads, "v_in", dev)
     if v_in.shape[0] != n:
         raise ValueError("k_pre and v_in must have as many tokens")
     rc = _lib.rtp_append_q8(cfg, cache, k, ks, v, vs, _arg(slot_map, torch.int64, "slot_map", dev, n),
@@ -312,8 +309,9 @@ def rtp_attn_q8(cfg, cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, 
     if workspace is None:
         raise ValueError("workspace is missing: rtp_attn_q8_workspace_bytes says how much")
     i32, dev, n, B = torch.int32, _device(q_pre, "q_pre"), q_pre.shape[0], cfg.batch
-    _check_pool(cache, cfg, dev)
-    q, qs = _packed(q_pre, cfg, cfg.n_q_heads, "q_pre", dev)
+    D = cfg.head_dim
+    _check_pool(cache, cfg.n_kv_heads, D, dev)
+    q, qs = _packed(q_pre, D, torch.bfloat16 if cfg.dtype == RTP_BF16 else torch.float32, cfg.n_q_heads, "q_pre", dev)
     if out.shape != q_pre.shape:
         raise ValueError("out must have q_pre's shape")
     if workspace.numel() < workspace_bytes:
@@ -339,7 +337,7 @@ class _Memory:
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(dev).synchronize()
 
-    def _on(self, stream, tensors) -> int:
+    def _on(self, stream) -> int:
         """The handle of a call's stream; torch is told of streams that it has not
         seen, so that freed memory waits for them (not of streams made elsewhere,
         which may be gone by then: synchronise those before the owner goes)."""
@@ -350,7 +348,7 @@ class _Memory:
                 s = torch.cuda.current_stream(self._dev) if stream is None else stream
                 if handle == 0 or s.stream_id != handle:  # (an outside stream's id is its handle)
                     self._streams[handle] = s
-                    for t in tensors:
+                    for t in self._tensors():
                         t.record_stream(s)
         return handle
 
@@ -403,12 +401,12 @@ class PagedLayer(_Memory):
         return self.k, self.v, self.k_scale, self.v_scale, self.status, self.ws
 
     def append(self, k_pre, v_in, slot_map, pos, stream=None) -> None:
-        rtp_append_q8(self.cfg, self.cache, k_pre, v_in, slot_map, pos, self.rope, self._on(stream, self._tensors()))
+        rtp_append_q8(self.cfg, self.cache, k_pre, v_in, slot_map, pos, self.rope, self._on(stream))
 
     def attend(self, q_pre, cu_q, seq_len, block_table, pos, out, max_q: int, max_seq_len: int = 0, stream=None) -> None:
         self.reserve(q_pre.shape[0], max_q, max_seq_len)
         rtp_attn_q8(self.cfg, self.cache, q_pre, cu_q, seq_len, block_table, pos, out, max_q, max_seq_len, self.rope,
-                    self.ws, self.ws.numel(), self._on(stream, self._tensors()))
+                    self.ws, self.ws.numel(), self._on(stream))
 
     def device_status(self) -> int:
         return int(self.status.item())
@@ -470,28 +468,28 @@ class Layer(_Memory):
             self.ws_prefill_bytes = n
             self.ws_prefill = self._scratch(n, self._dev)
 
-    def _call_stream(self, stream) -> int:
+    def _tensors(self):
         t = (self.k, self.v, self.kidx_full, self.status, self.ws_decode)
-        return self._on(stream, t if self.ws_prefill is None else t + (self.ws_prefill,))
+        return t if self.ws_prefill is None else t + (self.ws_prefill,)
 
     def append(self, k_pre, v_in, start_pos, w_k, stream=None) -> None:
-        rtp_append_kv(self.cfg, self.cache, k_pre, v_in, start_pos, k_pre.shape[1], w_k, self._call_stream(stream))
+        rtp_append_kv(self.cfg, self.cache, k_pre, v_in, start_pos, k_pre.shape[1], w_k, self._on(stream))
 
     def decode(self, q_pre, seq_len, w_q, out, max_seq_len: int = 0, sel_bitmask=None,
                sel_count=None, stream=None) -> None:
         rtp_decode_attn(self.cfg, self.cache, q_pre, seq_len, max_seq_len, w_q, out, sel_bitmask,
-                        sel_count, self.ws_decode, self.ws_decode_bytes, self._call_stream(stream))
+                        sel_count, self.ws_decode, self.ws_decode_bytes, self._on(stream))
 
     def recall(self, q_pre, seq_len, sel_bitmask, recall, max_seq_len: int = 0, stream=None) -> None:
         rtp_decode_recall(self.cfg, self.cache, q_pre, seq_len, max_seq_len, sel_bitmask, recall,
-                          self.ws_decode, self.ws_decode_bytes, self._call_stream(stream))
+                          self.ws_decode, self.ws_decode_bytes, self._on(stream))
 
     def prefill(self, q_pre, start_pos, w_q, out, sel_bitmask=None, sel_tau=None, sel_jcut=None,
                 sel_count=None, stream=None) -> None:
         T = q_pre.shape[1]
         self.reserve_prefill(T)
         rtp_prefill_attn(self.cfg, self.cache, q_pre, start_pos, T, w_q, out, sel_bitmask, sel_tau,
-                         sel_jcut, sel_count, self.ws_prefill, self.ws_prefill_bytes, self._call_stream(stream))
+                         sel_jcut, sel_count, self.ws_prefill, self.ws_prefill_bytes, self._on(stream))
 
     def device_status(self) -> int:
         return int(self.status.item())

@@ -17,20 +17,20 @@ def _cfg(**kw):
 def test_packed_rows_that_overlap_are_refused():
     """Above all a row that a broadcast repeats: its stride of 0 would mean
     dense rows to the library, which would read past the one row there is."""
-    cfg = _cfg()
+    dt = torch.bfloat16
     for name, heads in (("k_pre", 2), ("v_in", 2), ("q_pre", 8)):
         one = torch.zeros(1, heads, 64, dtype=torch.bfloat16)
         with pytest.raises(ValueError, match=name):
-            rtp._packed(one.expand(5, heads, 64), cfg, heads, name, -1)
+            rtp._packed(one.expand(5, heads, 64), 64, dt, heads, name, -1)
         flat = torch.zeros(heads * 64 * 5, dtype=torch.bfloat16)
         with pytest.raises(ValueError, match=name):
-            rtp._packed(flat.as_strided((3, heads, 64), (64, 64, 1)), cfg, heads, name, -1)
+            rtp._packed(flat.as_strided((3, heads, 64), (64, 64, 1)), 64, dt, heads, name, -1)
         # one row, dense rows, and slices of wider ones
-        assert rtp._packed(one, cfg, heads, name, -1) == (one.data_ptr(), 0)
-        assert rtp._packed(one.expand(1, heads, 64), cfg, heads, name, -1)[1] == 0
-        assert rtp._packed(torch.zeros(3, heads, 64, dtype=torch.bfloat16), cfg, heads, name, -1)[1] == heads * 64
+        assert rtp._packed(one, 64, dt, heads, name, -1) == (one.data_ptr(), 0)
+        assert rtp._packed(one.expand(1, heads, 64), 64, dt, heads, name, -1)[1] == 0
+        assert rtp._packed(torch.zeros(3, heads, 64, dtype=torch.bfloat16), 64, dt, heads, name, -1)[1] == heads * 64
         wide = torch.zeros(3, 12 * 64, dtype=torch.bfloat16)[:, 128:128 + heads * 64].unflatten(1, (heads, 64))
-        assert rtp._packed(wide, cfg, heads, name, -1)[1] == 12 * 64
+        assert rtp._packed(wide, 64, dt, heads, name, -1)[1] == 12 * 64
 
 
 class _FakeCuda:
@@ -56,11 +56,11 @@ def _pool(monkeypatch, heads=2, D=64, status=((1,), torch.int32), devices=(0,) *
 
 def test_a_pool_is_held_against_the_call(monkeypatch):
     cache = _pool(monkeypatch, devices=(1,) * 5)
-    rtp._check_pool(cache, _cfg(), 1)
-    for cfg, dev in ((_cfg(n_kv_heads=4), 1), (_cfg(n_kv_heads=1), 1), (_cfg(head_dim=128), 1), (_cfg(), 0)):
+    rtp._check_pool(cache, 2, 64, 1)
+    for heads, D, dev in ((4, 64, 1), (1, 64, 1), (2, 128, 1), (2, 64, 0)):
         with pytest.raises(ValueError, match="pool"):
-            rtp._check_pool(cache, cfg, dev)
-    rtp._check_pool(rtp.rtp_q8_cache(0, 0, 0, 0, 0, 3, 32), _cfg(), 0)  # bare addresses: the caller's word
+            rtp._check_pool(cache, heads, D, dev)
+    rtp._check_pool(rtp.rtp_q8_cache(0, 0, 0, 0, 0, 3, 32), 2, 64, 0)  # bare addresses: the caller's word
 
 
 def test_a_pool_of_several_devices_or_of_another_status_is_refused(monkeypatch):
