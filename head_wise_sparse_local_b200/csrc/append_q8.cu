@@ -16,8 +16,8 @@
 // The same holds for the scale: the maximum less and plus the largest e nearly
 // always name one power of two.
 //
-// Measured, 8K tokens of 8 heads, D = 128, bf16, three axes: 26 us (50 MB, 1.9
-// TB/s); 64 bits throughout, with a table of cosines in shared memory, took 36;
+// Measured in a replayed graph, 8K tokens of 8 heads, D = 128, bf16, three axes: 26 us
+// (50 MB, 1.9 TB/s); 64 bits throughout, with a table of cosines in shared memory, took 36;
 // the fp32 way with the cosines of a run shared through shared memory 29 to 40;
 // without any cosines, 19 to 21: what is left is the chain slots, rows, maximum,
 // store of each CTA with 16 warps an SM.

@@ -7,8 +7,9 @@
 //   x_j = q.k'_j ks / sqrt(D) log2(e) + log2(vs),   w_j = 2^(x_j - M),
 //   O = sum_j w_j v'_j,   l = sum_j w_j / vs_j,   out = O / l.
 // Taking vs into the exponent keeps the value blocks' scales out of the
-// products and the weights in (0, 1] whatever the scales are; M is the running
-// maximum of x, moved only when a tile exceeds it by 2^8.
+// products; M is the running maximum of x, moved only when a tile exceeds it by
+// 2^8, so weights are at most 2^8 whatever the scales are, and 2^14 as held in
+// fp16 (2^6 up), whose largest is 2^16 less 32.  l is another matter: see kAqFar.
 //
 // Work.  A tile is 32 positions of one (request, KV head, row chunk) item.  All
 // tiles of all items, and some units an item for its start and end, form one
@@ -35,10 +36,12 @@
 // conversions of about 1 clock.  (tcgen05 would spend as long: its 128-row operand would be
 // 8 or 16 rows full.)
 //
-// Measured, 32 query / 8 KV heads, D = 128, bf16, both kernels of a call: one
-// request at 1M positions 92 us (543 MB, 5.9 TB/s, 90% of a copy's rate), at 128K
-// 21 us (70 MB); 8 requests of 8K to 32K positions 24 us (95 MB), as drafts 39 us
-// (16 rows a chunk, so their tiles are read twice).
+// Measured, 32 query / 8 KV heads, D = 128, bf16, both kernels of a call in a
+// replayed graph (a call from a host program that makes one after another takes 1
+// to 3 us more): one request at 1M positions 92.5 us (543 MB, 5.9 TB/s, 90% of a
+// copy's rate), at 128K 20.7 us (70 MB); 8 requests of 8K to 32K positions 24.8 us
+// (95 MB), as drafts 39.2 us (16 rows a chunk, so their tiles are read twice).
+// Value scales of any size cost 0.2 of the 24.8 and 0.6 of the 39.2.
 #include "attn_q8.cuh"
 #include "tc.cuh"
 #include "tensor_map.h"

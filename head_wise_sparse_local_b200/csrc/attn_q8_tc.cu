@@ -46,8 +46,9 @@
 // clocks of the MUFU pipe, of which a quarter go to the FMA pipe (none: 399 us
 // for 384; an eighth 393; a half 421).
 //
-// Measured, 2K queries of 32 heads at 32K positions, D = 128: 365 us for the
-// three kernels (319 GFLOP, 870 TFLOP/s, 53% of a large matrix product's rate).
+// Measured, 2K queries of 32 heads at 32K positions, D = 128: 359 us for the
+// three kernels in a replayed graph (319 GFLOP, 890 TFLOP/s, 54% of a large matrix
+// product's rate).
 // A tile takes 4950 clocks: a slot's softmax 2700 of them, then its own two
 // products and the turn of the other slot's (1700), 250 from one to the next;
 // an item's end and start about as long as three tiles.

@@ -14,7 +14,7 @@
 // loads, the sums and a store); for large chunks the 12 bytes per token that
 // are written.
 //
-// Measured: 8 decoding requests 4.5 us; 256 requests that decode, end and bring
+// Measured in a replayed graph: 8 decoding requests 4.5 us; 256 requests that decode, end and bring
 // chunks 11 us (26 before a warp formed its sums by itself and a block was looked
 // up once for four tokens).
 #include "common.cuh"

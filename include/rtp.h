@@ -303,7 +303,8 @@ int rtp_prefill_attn(const rtp_layer_cfg* cfg, const rtp_cache* cache, const voi
  *
  * A block holds block_size consecutive positions of one request, for every KV
  * head, as e4m3 values with one fp32 scale per (block, KV head) for K and one
- * for V: half the bytes of a bf16 cache.  Scales are powers of two, so a
+ * for V: half the bytes of a bf16 cache that keeps every position of every head
+ * (a ring, rtp_layer_cfg.local_cap, keeps fewer of local heads and may be smaller).  Scales are powers of two, so a
  * stored value times its scale is exact in bf16 and fp32, and a block whose
  * scale grows keeps its values (only what falls below e4m3's smallest step is
  * rounded again).  A request's blocks may lie anywhere in the pool; its row of
