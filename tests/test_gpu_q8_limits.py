@@ -129,6 +129,8 @@ def test_scratch_is_not_memory_that_another_stream_still_uses(how):
 
 def test_memory_of_a_layer_that_goes_waits_for_its_streams():
     a = _Attn([1900, 400], [70, 1], D=64, bs=32, seed=24).device()
+    a.call()  # (loads the kernels)
+    a.out.zero_()
     s = torch.cuda.Stream()
     layer = _layer(a.dk.shape[0])
     layer.cache = a.cache
