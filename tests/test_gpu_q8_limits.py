@@ -357,6 +357,8 @@ class _Strict(_Attn):
         chunk = self.max_q * self.G > 32
         for b in range(self.B):
             L, n = self.lens[b], self.new[b]
+            if n == 0:
+                continue
             own = chunk and (n * self.G > 32 or self.B == 1)  # its kernel
             for hk in range(self.hkv):
                 k, v = self.pool.rows(self.table[b], L, hk)
