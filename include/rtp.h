@@ -304,7 +304,8 @@ int rtp_prefill_attn(const rtp_layer_cfg* cfg, const rtp_cache* cache, const voi
  * A block holds block_size consecutive positions of one request, for every KV
  * head, as e4m3 values with one fp32 scale per (block, KV head) for K and one
  * for V: half the bytes of a bf16 cache that keeps every position of every head
- * (a ring, rtp_layer_cfg.local_cap, keeps fewer of local heads and may be smaller).  Scales are powers of two, so a
+ * (a ring, rtp_layer_cfg.local_cap, keeps fewer of local heads' and may be
+ * smaller).  Scales are powers of two, so a
  * stored value times its scale is exact in bf16 and fp32, and a block whose
  * scale grows keeps its values (only what falls below e4m3's smallest step is
  * rounded again).  A request's blocks may lie anywhere in the pool; its row of
@@ -377,7 +378,7 @@ int rtp_q8_cache_bytes(const rtp_layer_cfg* cfg, int n_blocks, int block_size, s
  * entries from there on are no longer its own and would be lost.  The caller gives them
  * back before the next plan, by one in which they are a request of their own that ends:
  * batch rows of a table that begin with those entries, ctx_len[b] = block_size times
- * their number, new_len[b] = -1, max_tokens = 0.
+ * their number (max_ctx where that is less), new_len[b] = -1, max_tokens = 0.
  *
  * A request that cannot be served is refused: it takes no block, seq_len[b] =
  * ctx_len[b], its tokens get slot -1 (so rtp_append_q8 skips them), the others
@@ -386,8 +387,8 @@ int rtp_q8_cache_bytes(const rtp_layer_cfg* cfg, int n_blocks, int block_size, s
  * its packed tokens pass max_tokens (RTP_DEV_POSITION).  ctx_len[b] outside [0, max_ctx]
  * counts as 0 cached and no new tokens (RTP_DEV_SEQ_LEN).
  * rtp_attn_q8 knows nothing of refusals: a refused request keeps its rows in cu_new,
- * so its outputs there are made as if its newest cached tokens were the new ones, and
- * mean nothing.  Where *status has one of these bits, its rows are those with slot -1
+ * so its outputs there are made as if its newest cached tokens were the new ones (or
+ * left as they were, where it has fewer of them), and mean nothing.  Where *status has one of these bits, its rows are those with slot -1
  * ahead of cu_new[B]; the caller drops them, or plans the step again without it.
  *
  *   ctx_len, new_len  [B] int32, device
@@ -454,12 +455,14 @@ int rtp_attn_q8_workspace_bytes(const rtp_layer_cfg* cfg, int block_size, int n_
  *   out = softmax(RoPE(q, pos) . k_j / sqrt(D)) v_j    k_j, v_j as stored, times their scales
  * One token a request (decode), a few, or chunks, in any mix.  Arithmetic is
  * on tensor cores with fp32 accumulation; queries (scaled by a power of two a
- * row) and softmax weights enter them as fp16
- * (value scales of any size may lie beside one another; requests of more than
- * 32 query rows (n G) a KV head, in bf16, lose bits of query rows below 2^-64, and
- * want scores q . k / sqrt(D) of less than 2^23: larger ones may answer NaN).  Queries enter as two fp16 parts (22 bits)
- * where max_q * G <= 8, and for fp32 layers, whose weights do so too.  Blocks may be shared between requests.  v holds no NaN at cached
- * positions (rtp_append_q8 writes none): a weight of 0 does not hide one.
+ * row) and softmax weights enter them as fp16.  Queries enter as two fp16 parts
+ * (22 bits) where max_q * G <= 8, and for fp32 layers, whose weights do so too.
+ * Value scales of any size may lie beside one another.  Where max_q * G > 32, in
+ * bf16, requests of more than 32 query rows (n G) a KV head, and a batch of one,
+ * lose bits of query rows below 2^-64 and want scores q . k / sqrt(D) of less
+ * than 2^23: larger ones may answer NaN.  Blocks may be shared between requests.
+ * v holds no NaN at cached positions (rtp_append_q8 writes none): a weight of 0
+ * does not hide one.
  *
  *   q_pre        [n_tokens][Hq][D] dtype, device, pre-RoPE; rows q_stride
  *                elements apart (multiple of 16 bytes, at least Hq * D; 0 means Hq * D)

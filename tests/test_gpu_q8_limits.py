@@ -502,7 +502,7 @@ def test_lengths_that_fall_and_blocks_that_go_back():
         at = (keep[:, None] + torch.arange(cols, device=DEV)).clamp_max(cols - 1)
         none = torch.empty(0, dtype=torch.int32, device=DEV)
         scratch = torch.empty(3, dtype=torch.int32, device=DEV)
-        rtp.rtp_page_plan(s.layer.cfg, bs, ((had - keep) * bs).int(), torch.full_like(scratch, -1), s.table.gather(1, at.long()).contiguous(),
+        rtp.rtp_page_plan(s.layer.cfg, bs, ((had - keep) * bs).clamp_max(s.layer.cfg.max_ctx).int(), torch.full_like(scratch, -1), s.table.gather(1, at.long()).contiguous(),
                           s.free, s.n_free, scratch, torch.empty(4, dtype=torch.int32, device=DEV), none.long(), none, s.n_free, s.layer.status)
 
     s.step([30, 16, 47])
